@@ -34,6 +34,14 @@ Entry points (same names as the C ABI):
 * ``moe_dispatch_fused_replicated(x, expert_ids, num_experts, replica_offsets,
   replica_thresholds, seed)`` -> ``(replica_ids, Layout, expand_x[,
   quant_scales])`` (the replica-aware layout and the dispatch in one call)
+* ``moe_grouped_gemm_fp8(expand_x, quant_scales, weight, weight_scales,
+  expert_counts, ep_send_counts)`` -> ``out`` (the experts' product over
+  dispatched e4m3 rows, bf16 out; without counts one dense product)
+* ``moe_grouped_gemm_silu_fp8(...)`` -> ``(codes, scales)`` (the first product
+  of an expert with silu(gate) * up and the e4m3 quantisation of the result)
+* ``moe_combine_backward(grad_out, expand_x, ..., expert_scales)`` ->
+  ``(grad_expand_x, grad_expert_scales)``
+* ``moe_dispatch_backward(grad_expand_x, ..., grad_x_add=None)`` -> ``grad_x``
 * ``moe_plan_compensation(expert_counts, ep_world_size, tile_cost,
   activation_cost)`` -> dict (host-side 128-aligned chunk-migration plan)
 * ``moe_dispatch_capacity`` / ``moe_dispatch_layout_workspace_size``
@@ -64,7 +72,8 @@ __all__ = [
     "moe_dispatch_layout", "moe_dispatch_layout_ep", "moe_dispatch_layout_replicated",
     "moe_dispatch", "moe_dispatch_fused", "moe_dispatch_fused_replicated", "moe_combine",
     "moe_dispatch_fused_noalloc", "moe_noalloc_scratch_bytes",
-    "moe_plan_compensation",
+    "moe_grouped_gemm_fp8", "moe_grouped_gemm_silu_fp8", "moe_combine_backward",
+    "moe_dispatch_backward", "moe_plan_compensation",
     "moe_combine_fp8", "moe_probe_stream_mix", "moe_probe_empty", "moe_time_next_launches",
     "moe_time_unused_launches", "prepare", "Prepared",
     "MOE_BF16", "MOE_FP8_E4M3", "MOE_FLAG_ID_RANGE", "MOE_FLAG_DUP_ID", "MOE_FLAG_GUARD",
@@ -119,6 +128,14 @@ def load_library() -> ctypes.CDLL:
                                        P, P]),
         "moe_combine_fp8": (ctypes.c_int, [P, i64, i64, P, P, P, P, P, P, i64, i32, i32, i32,
                                            i32, P, P, P]),
+        "moe_grouped_gemm_fp8": (ctypes.c_int, [P, i64, i64, P, P, P, P, P, i32, i32, i32, i64, P,
+                                                i64, P, P]),
+        "moe_grouped_gemm_silu_fp8": (ctypes.c_int, [P, i64, i64, P, P, P, P, P, i32, i32, i32,
+                                                     i64, P, i64, P, P, P]),
+        "moe_combine_backward": (ctypes.c_int, [P, i64, P, i64, i64, P, P, P, P, i32, i32, i32,
+                                                i32, P, i64, P, P, P]),
+        "moe_dispatch_backward": (ctypes.c_int, [P, i64, i64, P, P, P, P, i64, i32, i32, i32, i32,
+                                                 P, P, P]),
         "moe_plan_compensation": (ctypes.c_int, [P, i32, i32, i64, i64, i64, i32, P, P, P, P, P,
                                                  P]),
         "moe_dispatch_layout_ep": (ctypes.c_int, [P, i32, i32, i32, i32, i32, P, P, P, P, P, P,
@@ -158,6 +175,32 @@ def _launch(fn, *args) -> int:
         calls.append((fn, args))
         return MOE_OK
     return fn(*args)
+
+
+# torch's device index getter is the cheapest one (some tens of ns); the null
+# stream belongs to the current device, so a call on another device's
+# tensors has to make that device current for its launch.
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+class _OnDevice:
+    """A library function whose launches go to device `dev`, whichever
+    device is current when it is called."""
+
+    def __init__(self, fn, dev: int):
+        self._fn = fn
+        self._dev = dev
+        self.argtypes = getattr(fn, "argtypes", None)
+
+    def __call__(self, *args):
+        if _get_device() == self._dev:
+            return self._fn(*args)
+        with torch.cuda.device(self._dev):
+            return self._fn(*args)
+
+
+def _on_device(fn, dev: int):
+    return _OnDevice(fn, dev) if dev >= 0 else fn
 
 
 class Prepared:
@@ -638,6 +681,216 @@ def moe_combine_fp8(expand_x: torch.Tensor, quant_scales: torch.Tensor, expert_i
     _check(rc)
     if check:
         _raise_on_status(status, "moe_combine_fp8")
+    return out
+
+
+def _product_rows(expand_x, quant_scales, weight, weight_scales, expert_counts, ep_send_counts,
+                  dev):
+    """The inputs of an experts' product, checked against each other; returns
+    (capacity_rows, row stride, experts, weight rows of one expert, channels)."""
+    stride = _row_stride(expand_x, "expand_x")
+    cap, channels = expand_x.shape
+    if channels == 0 or channels % 128:
+        raise ValueError("e4m3 rows need a positive multiple of 128 channels")
+    _need(quant_scales, torch.float32, "quant_scales", device=dev)
+    if tuple(quant_scales.shape) != (cap, channels // 128):
+        raise ValueError("quant_scales must be [capacity_rows, channels/128]")
+    _need(weight, torch.uint8, "weight", device=dev)
+    if weight.dim() != 3 or weight.shape[2] != channels:
+        raise ValueError(f"weight must be [E, N, {channels}], got {list(weight.shape)}")
+    experts, n, _ = weight.shape
+    _need(weight_scales, torch.float32, "weight_scales", device=dev)
+    if tuple(weight_scales.shape) != (experts, (n + 127) // 128, channels // 128):
+        raise ValueError("weight_scales must be [E, ceil(N/128), channels/128]")
+    if (expert_counts is None) != (ep_send_counts is None):
+        raise ValueError("expert_counts and ep_send_counts go together")
+    if expert_counts is None:
+        if experts != 1:
+            raise ValueError("a product without expert_counts takes one expert's weight")
+    else:
+        _need(expert_counts, torch.int32, "expert_counts", device=dev)
+        _need_len(expert_counts, experts, "expert_counts")
+        _need(ep_send_counts, torch.int32, "ep_send_counts", device=dev)
+        _need_len(ep_send_counts, experts + 1, "ep_send_counts")
+    return cap, stride, experts, n, channels
+
+
+def moe_grouped_gemm_fp8(expand_x: torch.Tensor, quant_scales: torch.Tensor,
+                         weight: torch.Tensor, weight_scales: torch.Tensor,
+                         expert_counts: Optional[torch.Tensor],
+                         ep_send_counts: Optional[torch.Tensor], *,
+                         expected_rows: Optional[int] = None,
+                         out: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None,
+                         check: bool = False) -> torch.Tensor:
+    """out[r] = weight[e] @ expand_x[r] for the rows r of each expert e, from
+    e4m3 codes (uint8) with fp32 scales: rows [cap, C] with [cap, C/128],
+    weights [E, N, C] with [E, ceil(N/128), C/128].  Returns bf16 [cap, N];
+    rows of no expert are not written.  expert_counts and ep_send_counts are
+    the layout's; None for both: one dense product of all rows (E = 1).
+    expected_rows (BS*K) chooses the launch shape, never the result; give it
+    when the buffer is much larger than the batch.  check=True waits for the
+    GPU and raises MoeStatusError if a segment leaves the buffer."""
+    dev = _need(expand_x, torch.uint8, "expand_x", contiguous=False)
+    cap, xs, experts, n, channels = _product_rows(expand_x, quant_scales, weight, weight_scales,
+                                                  expert_counts, ep_send_counts, dev)
+    if out is None:
+        out = _new((cap, n), torch.bfloat16, dev)
+    _need(out, torch.bfloat16, "out", contiguous=False, device=dev)
+    out_stride = _need_rows(out, cap, n, "out")
+    status = _status_word(status, check, dev)
+    rc = _launch(_on_device(load_library().moe_grouped_gemm_fp8, dev),
+        _ptr(expand_x), xs, cap, _ptr(quant_scales), _ptr(weight), _ptr(weight_scales),
+        _ptr(expert_counts), _ptr(ep_send_counts), experts, channels, n,
+        _expected(expected_rows), _ptr(out), out_stride, _ptr(status), _stream(expand_x))
+    _check(rc)
+    if check:
+        _raise_on_status(status, "moe_grouped_gemm_fp8")
+    return out
+
+
+def _expected(expected_rows: Optional[int]) -> int:
+    if expected_rows is None:
+        return 0
+    if expected_rows < 0:
+        raise ValueError("expected_rows must be >= 0")
+    return expected_rows
+
+
+def moe_grouped_gemm_silu_fp8(expand_x: torch.Tensor, quant_scales: torch.Tensor,
+                              weight: torch.Tensor, weight_scales: torch.Tensor,
+                              expert_counts: Optional[torch.Tensor],
+                              ep_send_counts: Optional[torch.Tensor], *,
+                              expected_rows: Optional[int] = None,
+                              out: Optional[torch.Tensor] = None,
+                              out_scales: Optional[torch.Tensor] = None,
+                              status: Optional[torch.Tensor] = None, check: bool = False):
+    """The experts' first product with its gated activation, quantised for the
+    second: weight [E, 2*I, C] holds the I gate rows, then the I up rows, of
+    each expert; h = silu(gate) * up in fp32, then e4m3 codes (uint8 [cap, I])
+    and fp32 scales [cap, I/128].  Returns ``(codes, scales)``; other
+    arguments as for moe_grouped_gemm_fp8."""
+    dev = _need(expand_x, torch.uint8, "expand_x", contiguous=False)
+    cap, xs, experts, n, channels = _product_rows(expand_x, quant_scales, weight, weight_scales,
+                                                  expert_counts, ep_send_counts, dev)
+    if n == 0 or n % 256:
+        raise ValueError("weight must hold 2*I rows an expert, I a positive multiple of 128")
+    inter = n // 2
+    if out is None:
+        out = _new((cap, inter), torch.uint8, dev)
+    _need(out, torch.uint8, "out", contiguous=False, device=dev)
+    out_stride = _need_rows(out, cap, inter, "out")
+    if out_scales is None:
+        out_scales = _new((cap, inter // 128), torch.float32, dev)
+    _need(out_scales, torch.float32, "out_scales", device=dev)
+    _need_rows(out_scales, cap, inter // 128, "out_scales")
+    status = _status_word(status, check, dev)
+    rc = _launch(_on_device(load_library().moe_grouped_gemm_silu_fp8, dev),
+        _ptr(expand_x), xs, cap, _ptr(quant_scales), _ptr(weight), _ptr(weight_scales),
+        _ptr(expert_counts), _ptr(ep_send_counts), experts, channels, inter,
+        _expected(expected_rows), _ptr(out), out_stride, _ptr(out_scales), _ptr(status),
+        _stream(expand_x))
+    _check(rc)
+    if check:
+        _raise_on_status(status, "moe_grouped_gemm_silu_fp8")
+    return out, out_scales
+
+
+def moe_combine_backward(grad_out: torch.Tensor, expand_x: Optional[torch.Tensor],
+                         expert_ids: torch.Tensor, expand_idx: torch.Tensor,
+                         ep_send_counts: torch.Tensor, expert_scales: torch.Tensor,
+                         num_experts: int, *, need_expand_x: bool = True,
+                         need_scales: bool = True, capacity_rows: Optional[int] = None,
+                         grad_expand_x: Optional[torch.Tensor] = None,
+                         grad_expert_scales: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None, check: bool = False):
+    """Gradient of moe_combine: ``(grad_expand_x, grad_expert_scales)`` from
+    grad_out [BS, H] bf16 and the combine's own inputs; the shared row's
+    gradient is grad_out itself.  grad_expand_x [cap, H] bf16 holds
+    expert_scales[t,j] * grad_out[t] at each pair's row (rows of no pair are
+    not written; pass expand_x itself to overwrite it), grad_expert_scales
+    [BS, K] fp32 the dot products.  An output not needed is None; without
+    need_scales expand_x may be None (then capacity_rows or grad_expand_x
+    gives the rows)."""
+    dev = _need(grad_out, torch.bfloat16, "grad_out", contiguous=False)
+    if grad_out.dim() != 2:
+        raise ValueError("grad_out must be [BS, H]")
+    bs, hidden = grad_out.shape
+    k = _routes(expert_ids, expand_idx, ep_send_counts, num_experts, bs, dev)
+    _need(expert_scales, torch.float32, "expert_scales", device=dev)
+    _need_len(expert_scales, bs * k, "expert_scales")
+    if not need_expand_x and not need_scales:
+        raise ValueError("need_expand_x or need_scales must be set")
+    if expand_x is None and need_scales:
+        raise ValueError("expand_x is needed for grad_expert_scales")
+    if capacity_rows is None:
+        rows = expand_x if expand_x is not None else grad_expand_x
+        if rows is None:
+            raise ValueError("capacity_rows, expand_x or grad_expand_x must give the rows")
+        capacity_rows = rows.shape[0]
+    if capacity_rows < 0:
+        raise ValueError("capacity_rows must be >= 0")
+    ys = dys = 0
+    if need_scales:
+        _need(expand_x, torch.bfloat16, "expand_x", contiguous=False, device=dev)
+        ys = _need_rows(expand_x, capacity_rows, hidden, "expand_x")
+        if grad_expert_scales is None:
+            grad_expert_scales = _new((bs, k), torch.float32, dev)
+        _need(grad_expert_scales, torch.float32, "grad_expert_scales", device=dev)
+        if tuple(grad_expert_scales.shape) != (bs, k):
+            raise ValueError(f"grad_expert_scales must be [{bs}, {k}]")
+    else:
+        grad_expert_scales = None
+    if need_expand_x:
+        if grad_expand_x is None:
+            grad_expand_x = _new((capacity_rows, hidden), torch.bfloat16, dev)
+        _need(grad_expand_x, torch.bfloat16, "grad_expand_x", contiguous=False, device=dev)
+        dys = _need_rows(grad_expand_x, capacity_rows, hidden, "grad_expand_x")
+    else:
+        grad_expand_x = None
+    status = _status_word(status, check, dev)
+    rc = _launch(_on_device(load_library().moe_combine_backward, dev),
+        _ptr(grad_out), _row_stride(grad_out, "grad_out"),
+        _ptr(expand_x) if need_scales else None, ys, capacity_rows, _ptr(expert_ids),
+        _ptr(expand_idx), _ptr(ep_send_counts), _ptr(expert_scales), bs, hidden, k, num_experts,
+        _ptr(grad_expand_x), dys, _ptr(grad_expert_scales), _ptr(status), _stream(grad_out))
+    _check(rc)
+    if check:
+        _raise_on_status(status, "moe_combine_backward")
+    return grad_expand_x, grad_expert_scales
+
+
+def moe_dispatch_backward(grad_expand_x: torch.Tensor, expert_ids: torch.Tensor,
+                          expand_idx: torch.Tensor, ep_send_counts: torch.Tensor,
+                          num_experts: int, *, grad_x_add: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None,
+                          status: Optional[torch.Tensor] = None,
+                          check: bool = False) -> torch.Tensor:
+    """Gradient of moe_dispatch: grad_x[t] = sum_j grad_expand_x[slot(t,j)]
+    (+ grad_x_add[t], what reaches the token on other paths), summed in fp32
+    and rounded once to bf16 [BS, H]."""
+    dev = _need(grad_expand_x, torch.bfloat16, "grad_expand_x", contiguous=False)
+    bs, k = _need_ids(expert_ids, device=dev)
+    _routes(expert_ids, expand_idx, ep_send_counts, num_experts, bs, dev)
+    gs = _row_stride(grad_expand_x, "grad_expand_x")
+    cap, hidden = grad_expand_x.shape
+    add_stride = 0
+    if grad_x_add is not None:
+        _need(grad_x_add, torch.bfloat16, "grad_x_add", contiguous=False, device=dev)
+        add_stride = _need_rows(grad_x_add, bs, hidden, "grad_x_add")
+    if out is None:
+        out = _new((bs, hidden), torch.bfloat16, dev)
+    _need(out, torch.bfloat16, "out", device=dev)
+    if tuple(out.shape) != (bs, hidden):
+        raise ValueError(f"out must be [{bs}, {hidden}], got {list(out.shape)}")
+    status = _status_word(status, check, dev)
+    rc = _launch(_on_device(load_library().moe_dispatch_backward, dev),
+        _ptr(grad_expand_x), gs, cap, _ptr(expert_ids), _ptr(expand_idx), _ptr(ep_send_counts),
+        _ptr(grad_x_add), add_stride, bs, hidden, k, num_experts, _ptr(out), _ptr(status),
+        _stream(grad_expand_x))
+    _check(rc)
+    if check:
+        _raise_on_status(status, "moe_dispatch_backward")
     return out
 
 

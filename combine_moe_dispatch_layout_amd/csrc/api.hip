@@ -28,6 +28,11 @@ bool is_pow2(int32_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// A pointer that is there and aligned to 4 bytes.
+bool aligned4(const void* p) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+
 int64_t capacity_rows_for(int32_t bs, int32_t k, int32_t num_experts, int32_t align) {
   const int64_t n = (int64_t)bs * k;
   const int64_t used = n < num_experts ? n : num_experts;
@@ -132,6 +137,32 @@ int layout_then_scatter(const void* x, int64_t x_stride, int32_t bs, int32_t hid
   return hip_status(moe::launch_dispatch_fp8(x, x_stride, bs, hidden, route_ids, ranks, send, k,
                                              ranked, expand_x, expand_x_stride, capacity_rows,
                                              quant_scales, status, s, dr));
+}
+
+// Rules of the experts' products, and their launch.  Either both of counts
+// and send are given, or neither (one group of all rows).
+int product_call(const moe::GroupedGemm& g, void* stream) {
+  const int32_t rows_per_expert = g.gated ? 2 : 1;
+  if (g.num_experts < 1 || g.num_experts > moe::kMaxExperts) return MOE_ERR_INVALID_ARG;
+  if ((g.counts == nullptr) != (g.send == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (g.counts == nullptr && g.num_experts != 1) return MOE_ERR_INVALID_ARG;
+  if (g.in_features <= 0 || g.in_features % 128 != 0 || g.in_features > 65536)
+    return MOE_ERR_INVALID_ARG;
+  if (g.out_features <= 0 || g.out_features % (g.gated ? 128 : 32) != 0 ||
+      g.out_features > 65536 / rows_per_expert)
+    return MOE_ERR_INVALID_ARG;
+  if (g.capacity_rows < 0 || g.capacity_rows > moe::kMaxRows || g.expected_rows < 0)
+    return MOE_ERR_INVALID_ARG;
+  if (g.capacity_rows == 0) return MOE_OK;
+  if (!row_ok(g.x, g.x_stride, g.in_features, 1)) return MOE_ERR_INVALID_ARG;
+  if (!row_ok(g.out, g.out_stride, g.out_features, g.gated ? 1 : 2)) return MOE_ERR_INVALID_ARG;
+  if (g.w == nullptr || !aligned16(g.w)) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(g.x_scales) || !aligned4(g.w_scales)) return MOE_ERR_INVALID_ARG;
+  if (g.gated && !aligned4(g.out_scales)) return MOE_ERR_INVALID_ARG;
+  moe::GroupedGemm call = g;
+  if (call.expected_rows == 0 || call.expected_rows > g.capacity_rows)
+    call.expected_rows = g.capacity_rows;
+  return hip_status(moe::launch_grouped_gemm(call, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace
@@ -416,6 +447,115 @@ int moe_combine_fp8(const void* expand_x, int64_t expand_x_stride, int64_t capac
                                             ep_send_counts, expert_scales, shared_expert_x,
                                             shared_stride, bs, hidden, k, num_experts, x_out,
                                             status, static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine_backward(const void* grad_out, int64_t grad_out_stride, const void* expand_x,
+                         int64_t expand_x_stride, int64_t capacity_rows,
+                         const int32_t* expert_ids, const int32_t* expand_idx,
+                         const int32_t* ep_send_counts, const float* expert_scales, int32_t bs,
+                         int32_t hidden, int32_t k, int32_t num_experts, void* grad_expand_x,
+                         int64_t grad_expand_x_stride, float* grad_expert_scales,
+                         int32_t* status, void* stream) {
+  if (!layout_args_ok(bs, k, num_experts, 1)) return MOE_ERR_INVALID_ARG;
+  if (hidden <= 0 || hidden % 32 != 0 || hidden > 65536) return MOE_ERR_INVALID_ARG;
+  if (capacity_rows < 0 || !rows_fit(bs, hidden)) return MOE_ERR_INVALID_ARG;
+  if (bs == 0) return MOE_OK;
+  if (capacity_rows > 0 && grad_expand_x == nullptr && grad_expert_scales == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (expert_ids == nullptr || expand_idx == nullptr || ep_send_counts == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (!row_ok(grad_out, grad_out_stride, hidden, 2)) return MOE_ERR_INVALID_ARG;
+  if (grad_expand_x != nullptr) {
+    if (!aligned4(expert_scales)) return MOE_ERR_INVALID_ARG;
+    if (!row_ok(grad_expand_x, grad_expand_x_stride, hidden, 2)) return MOE_ERR_INVALID_ARG;
+  }
+  if (grad_expert_scales != nullptr) {
+    if (!aligned4(grad_expert_scales)) return MOE_ERR_INVALID_ARG;
+    if (capacity_rows > 0 && !row_ok(expand_x, expand_x_stride, hidden, 2))
+      return MOE_ERR_INVALID_ARG;
+  }
+  return hip_status(moe::launch_combine_backward(
+      grad_out, grad_out_stride, expand_x, expand_x_stride, capacity_rows, expert_ids, expand_idx,
+      ep_send_counts, expert_scales, bs, hidden, k, num_experts, grad_expand_x,
+      grad_expand_x_stride, grad_expert_scales, status, static_cast<hipStream_t>(stream)));
+}
+
+int moe_dispatch_backward(const void* grad_expand_x, int64_t grad_expand_x_stride,
+                          int64_t capacity_rows, const int32_t* expert_ids,
+                          const int32_t* expand_idx, const int32_t* ep_send_counts,
+                          const void* grad_x_add, int64_t grad_x_add_stride, int32_t bs,
+                          int32_t hidden, int32_t k, int32_t num_experts, void* grad_x,
+                          int32_t* status, void* stream) {
+  if (!layout_args_ok(bs, k, num_experts, 1)) return MOE_ERR_INVALID_ARG;
+  if (hidden <= 0 || hidden % 32 != 0 || hidden > 65536) return MOE_ERR_INVALID_ARG;
+  if (capacity_rows < 0 || !rows_fit(bs, hidden)) return MOE_ERR_INVALID_ARG;
+  if (bs == 0) return MOE_OK;
+  if (expert_ids == nullptr || expand_idx == nullptr || ep_send_counts == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (capacity_rows > 0 && !row_ok(grad_expand_x, grad_expand_x_stride, hidden, 2))
+    return MOE_ERR_INVALID_ARG;
+  if (grad_x_add != nullptr &&
+      (grad_x_add == grad_x || !row_ok(grad_x_add, grad_x_add_stride, hidden, 2)))
+    return MOE_ERR_INVALID_ARG;
+  if (!row_ok(grad_x, hidden, hidden, 2)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_combine(grad_expand_x, grad_expand_x_stride, capacity_rows,
+                                        expert_ids, expand_idx, ep_send_counts, nullptr,
+                                        grad_x_add, grad_x_add_stride, bs, hidden, k,
+                                        num_experts, grad_x, status,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int moe_grouped_gemm_fp8(const void* expand_x, int64_t expand_x_stride, int64_t capacity_rows,
+                         const float* quant_scales, const void* weight,
+                         const float* weight_scales, const int32_t* expert_counts,
+                         const int32_t* ep_send_counts, int32_t num_experts,
+                         int32_t in_features, int32_t out_features, int64_t expected_rows,
+                         void* out, int64_t out_stride, int32_t* status, void* stream) {
+  moe::GroupedGemm g;
+  g.x = expand_x;
+  g.x_stride = expand_x_stride;
+  g.capacity_rows = capacity_rows;
+  g.x_scales = quant_scales;
+  g.w = weight;
+  g.w_scales = weight_scales;
+  g.counts = expert_counts;
+  g.send = ep_send_counts;
+  g.num_experts = num_experts;
+  g.in_features = in_features;
+  g.out_features = out_features;
+  g.expected_rows = expected_rows;
+  g.out = out;
+  g.out_stride = out_stride;
+  g.status = status;
+  return product_call(g, stream);
+}
+
+int moe_grouped_gemm_silu_fp8(const void* expand_x, int64_t expand_x_stride,
+                              int64_t capacity_rows, const float* quant_scales,
+                              const void* weight, const float* weight_scales,
+                              const int32_t* expert_counts, const int32_t* ep_send_counts,
+                              int32_t num_experts, int32_t in_features, int32_t inter_features,
+                              int64_t expected_rows, void* out, int64_t out_stride,
+                              float* out_scales, int32_t* status, void* stream) {
+  moe::GroupedGemm g;
+  g.x = expand_x;
+  g.x_stride = expand_x_stride;
+  g.capacity_rows = capacity_rows;
+  g.x_scales = quant_scales;
+  g.w = weight;
+  g.w_scales = weight_scales;
+  g.counts = expert_counts;
+  g.send = ep_send_counts;
+  g.num_experts = num_experts;
+  g.in_features = in_features;
+  g.out_features = inter_features;
+  g.expected_rows = expected_rows;
+  g.gated = true;
+  g.out = out;
+  g.out_stride = out_stride;
+  g.out_scales = out_scales;
+  g.status = status;
+  return product_call(g, stream);
 }
 
 int moe_time_next_launches(void* const* start_events, void* const* stop_events, int32_t n) {

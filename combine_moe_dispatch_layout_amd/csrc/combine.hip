@@ -21,7 +21,9 @@ namespace {
 // is one round trip (the decode step in graphs went from 14.6 to 12.9 us;
 // staging one load at a time, as the scatter does in large grids, changed
 // the 4096- and 16384-token combines by less than their run-to-run spread).
-template <int THREADS, int VPT, int KMAX>
+// Without WEIGHTED every weight is 1 (the gradient of the scatter) and scales
+// is not read.
+template <int THREADS, int VPT, int KMAX, bool WEIGHTED>
 __global__ __launch_bounds__(THREADS) void combine_kernel(
     const u32x4* __restrict__ y, int64_t ys, int64_t cap, const int32_t* __restrict__ ids,
     const int32_t* __restrict__ idx, const int32_t* __restrict__ send,
@@ -32,7 +34,7 @@ __global__ __launch_bounds__(THREADS) void combine_kernel(
   const int32_t t = blockIdx.x / nchunks;
   const int32_t chunk = blockIdx.x - t * nchunks;
   PairMeta meta;
-  fetch_pair_meta(meta, t, k, ids, idx, scales);
+  fetch_pair_meta(meta, t, k, ids, idx, WEIGHTED ? scales : nullptr);
   // The shared row does not depend on the routes.  Every lane loads it (a
   // lane past the row end repeats its last vector, and without a shared row
   // all lanes read a zero vector), so no branch separates these loads from
@@ -76,8 +78,9 @@ __global__ __launch_bounds__(THREADS) void combine_kernel(
       if (slot[j] < 0) continue;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        acc[2 * c] = __builtin_fmaf(w[j], bf16lo_to_f32(yv[jv][j][c]), acc[2 * c]);
-        acc[2 * c + 1] = __builtin_fmaf(w[j], bf16hi_to_f32(yv[jv][j][c]), acc[2 * c + 1]);
+        const float wj = WEIGHTED ? w[j] : 1.0f;
+        acc[2 * c] = __builtin_fmaf(wj, bf16lo_to_f32(yv[jv][j][c]), acc[2 * c]);
+        acc[2 * c + 1] = __builtin_fmaf(wj, bf16hi_to_f32(yv[jv][j][c]), acc[2 * c + 1]);
       }
     }
     if (shared) {
@@ -179,14 +182,14 @@ __global__ __launch_bounds__(1024) void combine_fp8_kernel(
   store_stream(o1, dst + 1);
 }
 
-template <int THREADS, int VPT>
+template <int THREADS, int VPT, bool WEIGHTED>
 hipError_t launch_t(int kmax, dim3 grid, const u32x4* y, int64_t ys, int64_t cap,
                     const int32_t* ids, const int32_t* idx, const int32_t* send,
                     const float* scales, const u32x4* shared, int64_t ss, int32_t nvec,
                     int32_t nchunks, int32_t k, int32_t E, u32x4* out,
                     int32_t* status, hipStream_t stream) {
 #define MOE_COMBINE(KM)                                                                   \
-  launch_kernel(combine_kernel<THREADS, VPT, KM>, grid, THREADS, stream, y, ys, cap,       \
+  launch_kernel(combine_kernel<THREADS, VPT, KM, WEIGHTED>, grid, THREADS, stream, y, ys, cap, \
       ids, idx, send, scales, shared, ss, nvec, nchunks, k, E, out, status)
   switch (kmax) {
     case 2: MOE_COMBINE(2); break;
@@ -212,11 +215,10 @@ hipError_t launch_combine(const void* y, int64_t y_stride, int64_t capacity_rows
   const int32_t n_items = bs * nchunks;
   const dim3 grid((uint32_t)n_items);
   const int kmax = k <= 2 ? 2 : k <= 4 ? 4 : k <= 8 ? 8 : 16;
-  return launch_t<kThreads, kVpt>(kmax, grid, static_cast<const u32x4*>(y), y_stride / 8,
-                                  capacity_rows, ids, expand_idx, send, scales,
-                                  static_cast<const u32x4*>(shared), shared_stride / 8, nvec,
-                                  nchunks, k, num_experts, static_cast<u32x4*>(out), status,
-                                  stream);
+  const auto launch = scales ? launch_t<kThreads, kVpt, true> : launch_t<kThreads, kVpt, false>;
+  return launch(kmax, grid, static_cast<const u32x4*>(y), y_stride / 8, capacity_rows, ids,
+                expand_idx, send, scales, static_cast<const u32x4*>(shared), shared_stride / 8,
+                nvec, nchunks, k, num_experts, static_cast<u32x4*>(out), status, stream);
 }
 
 }  // namespace moe

@@ -435,4 +435,34 @@ hipError_t launch_combine_fp8(const void* y, int64_t y_stride, int64_t capacity_
                               int32_t bs, int32_t hidden, int32_t k, int32_t num_experts,
                               void* out, int32_t* status, hipStream_t stream);
 
+// ---- gradient of dispatch and combine --------------------------------------
+hipError_t launch_combine_backward(const void* grad_out, int64_t grad_stride, const void* y,
+                                   int64_t y_stride, int64_t capacity_rows, const int32_t* ids,
+                                   const int32_t* expand_idx, const int32_t* send,
+                                   const float* scales, int32_t bs, int32_t hidden, int32_t k,
+                                   int32_t num_experts, void* grad_y, int64_t grad_y_stride,
+                                   float* grad_scales, int32_t* status, hipStream_t stream);
+
+// ---- the experts' products --------------------------------------------------
+struct GroupedGemm {
+  const void* x = nullptr;            // e4m3 rows [capacity_rows, in_features]
+  int64_t x_stride = 0;               // in bytes
+  int64_t capacity_rows = 0;
+  const float* x_scales = nullptr;    // [capacity_rows, in_features / 128]
+  const void* w = nullptr;            // e4m3 [num_experts, N, in_features]
+  const float* w_scales = nullptr;    // [num_experts, ceil(N / 128), in_features / 128]
+  const int32_t* counts = nullptr;    // [num_experts], or null: one group of every row
+  const int32_t* send = nullptr;      // [num_experts + 1]
+  int32_t num_experts = 0;
+  int32_t in_features = 0;
+  int32_t out_features = 0;           // N, or N / 2 with `gated`
+  int64_t expected_rows = 0;          // chooses the grid and the tile; any value is correct
+  bool gated = false;
+  void* out = nullptr;                // bf16 rows, or e4m3 codes with `gated`
+  int64_t out_stride = 0;             // in elements
+  float* out_scales = nullptr;        // [capacity_rows, out_features / 128] with `gated`
+  int32_t* status = nullptr;
+};
+hipError_t launch_grouped_gemm(const GroupedGemm& g, hipStream_t stream);
+
 }  // namespace moe

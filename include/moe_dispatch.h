@@ -415,6 +415,155 @@ int moe_dispatch_fused_replicated(const void* x, int64_t x_stride, int32_t bs, i
                                   void* stream);
 
 /*
+ * The experts' product over dispatched rows, in e4m3 with block scales: the
+ * grouped GEMM that the 128-row tiles of the layout are made for (TEMPO
+ * summary, section 1).  For the rows r of expert e, that is
+ * ep_send_counts[e] <= r < ep_send_counts[e] + expert_counts[e]:
+ *
+ *   out[r, n] = bf16( sum_b quant_scales[r, b] * weight_scales[e, n/128, b]
+ *                       * sum_{c in block b} expand_x[r, c] * weight[e, n, c] )
+ *
+ * over the 128-channel blocks b of a row, ascending.  Products of codes are
+ * exact and the running sum is fp32 (a fused multiply-add per block).  A
+ * block's own sum is the e4m3 matrix instruction's: it aligns each group of
+ * 8 products to the largest and keeps 13 bits below that one's leading bit,
+ * then adds in fp32 (measured on N(0,1) rows: 1.3e-5 of the result, against
+ * 2e-3 for its one rounding to bf16, to nearest even, at the end).  Rows of no expert (padding,
+ * and rows behind the last segment) are neither read nor written.  The
+ * result of a row does not depend on the other rows or on expected_rows.
+ * Scales and codes are taken as they are: a NaN code or a non-finite scale
+ * reaches every output that uses it.  The gradient of expand_x is the same
+ * call with the weights transposed (128 x 128 blocks transpose with them).
+ *
+ *  expand_x       in  e4m3fn codes [capacity_rows, in_features], row stride
+ *                     expand_x_stride bytes (>= in_features, a multiple of
+ *                     16), 16-byte aligned: moe_dispatch's e4m3 output.
+ *  capacity_rows  in  rows of expand_x and out, >= 0, at most 2^30.
+ *  quant_scales   in  fp32 [capacity_rows, in_features/128] row-major.
+ *  weight         in  e4m3fn codes [num_experts, out_features, in_features],
+ *                     contiguous, 16-byte aligned.
+ *  weight_scales  in  fp32 [num_experts, ceil(out_features/128),
+ *                     in_features/128]: one per 128 x 128 block of weight.
+ *  expert_counts, ep_send_counts
+ *                 in  the layout's outputs (any align).  Both NULL: one
+ *                     group of all capacity_rows rows (num_experts must be
+ *                     1), the dense product of a shared expert.
+ *  num_experts    in  1 <= num_experts <= 512.
+ *  in_features    in  a positive multiple of 128, at most 65536.
+ *  out_features   in  a positive multiple of 32, at most 65536.
+ *  expected_rows  in  about how many rows the experts have together (BS*K of
+ *                     the batch; 0: unknown, capacity_rows is taken).  It
+ *                     chooses launch and tile shapes, never the result.
+ *  out            out bf16 [capacity_rows, out_features], row stride
+ *                     out_stride elements, 16-byte aligned, stride*2 % 16 ==
+ *                     0; must not overlap an input.
+ *  status         in/out int32 [1] or NULL: MOE_FLAG_GUARD is OR-ed in when
+ *                     a segment leaves [0, capacity_rows) (the rows outside
+ *                     are skipped) or segments overlap so far that they hold
+ *                     more rows than the buffer (then nothing is written).
+ */
+int moe_grouped_gemm_fp8(const void* expand_x, int64_t expand_x_stride, int64_t capacity_rows,
+                         const float* quant_scales, const void* weight,
+                         const float* weight_scales, const int32_t* expert_counts,
+                         const int32_t* ep_send_counts, int32_t num_experts,
+                         int32_t in_features, int32_t out_features, int64_t expected_rows,
+                         void* out, int64_t out_stride, int32_t* status, void* stream);
+
+/*
+ * The experts' first product with its gated activation and the quantisation
+ * for the second product in one launch.  With z the product of
+ * moe_grouped_gemm_fp8 over weight rows [0, 2*inter_features), gate rows
+ * first, all of its sums in full fp32 (the codes are widened to fp16 for the
+ * matrix unit, since out_scales is an fp32 result) and not rounded:
+ *
+ *   h[r, c] = z[r, c] / (1 + exp(-z[r, c])) * z[r, inter_features + c]
+ *   out_scales[r, b] = max_{c in block b} |h[r, c]| / 448
+ *   out[r, c] = e4m3( h[r, c] / out_scales[r, b] ), nearest even, saturated
+ *
+ * over 128-channel blocks b: the format moe_dispatch emits, so out and
+ * out_scales are the next product's expand_x and quant_scales.  A block
+ * whose scale is 0 has codes 0; a block that holds an infinity or a NaN has
+ * that as its scale and NaN codes.
+ *
+ *  weight         in  e4m3fn codes [num_experts, 2*inter_features,
+ *                     in_features]; weight_scales fp32 [num_experts,
+ *                     2*inter_features/128, in_features/128].
+ *  inter_features in  a positive multiple of 128, at most 32768.
+ *  out            out e4m3fn codes [capacity_rows, inter_features], row
+ *                     stride out_stride bytes, a multiple of 16; 16-byte
+ *                     aligned.
+ *  out_scales     out fp32 [capacity_rows, inter_features/128] row-major.
+ *  other arguments as for moe_grouped_gemm_fp8.
+ */
+int moe_grouped_gemm_silu_fp8(const void* expand_x, int64_t expand_x_stride,
+                              int64_t capacity_rows, const float* quant_scales,
+                              const void* weight, const float* weight_scales,
+                              const int32_t* expert_counts, const int32_t* ep_send_counts,
+                              int32_t num_experts, int32_t in_features, int32_t inter_features,
+                              int64_t expected_rows, void* out, int64_t out_stride,
+                              float* out_scales, int32_t* status, void* stream);
+
+/*
+ * Gradient of moe_combine.  With g = grad_out (dL/dx_out):
+ *
+ *   grad_expand_x[slot(t,j), :] = bf16( expert_scales[t,j] * g[t, :] )
+ *   grad_expert_scales[t,j]     = sum_h g[t,h] * expand_x[slot(t,j), h]   (fp32)
+ *
+ * The gradient of shared_expert_x is g itself.  A pair that the combine
+ * skipped (id out of range, expand_idx < 0, slot beyond capacity_rows) has
+ * grad_expert_scales 0 and no row; rows of no pair are not written.  The
+ * sums' order is fixed, so results repeat bit for bit.
+ *
+ *  grad_out       in  bf16 [bs, hidden], row stride grad_out_stride; 16-byte
+ *                     aligned, stride*2 % 16 == 0 (as every row buffer here).
+ *  expand_x       in  the combine's input (read for grad_expert_scales only;
+ *                     may be NULL without it).
+ *  expert_ids, expand_idx, ep_send_counts, expert_scales, bs, hidden, k,
+ *  num_experts, capacity_rows
+ *                 in  as for moe_combine (expert_scales is read for
+ *                     grad_expand_x only).
+ *  grad_expand_x  out bf16 [capacity_rows, hidden], or NULL: not wanted.  May
+ *                     be expand_x itself (same address and stride): each
+ *                     element is read before it is overwritten.
+ *  grad_expert_scales
+ *                 out fp32 [bs, k] row-major, or NULL: not wanted.  One of
+ *                     the two outputs must be given (unless capacity_rows
+ *                     is 0).
+ *  status         in/out int32 [1] or NULL, as for moe_combine.
+ */
+int moe_combine_backward(const void* grad_out, int64_t grad_out_stride, const void* expand_x,
+                         int64_t expand_x_stride, int64_t capacity_rows,
+                         const int32_t* expert_ids, const int32_t* expand_idx,
+                         const int32_t* ep_send_counts, const float* expert_scales, int32_t bs,
+                         int32_t hidden, int32_t k, int32_t num_experts, void* grad_expand_x,
+                         int64_t grad_expand_x_stride, float* grad_expert_scales,
+                         int32_t* status, void* stream);
+
+/*
+ * Gradient of moe_dispatch with respect to the token rows: every row a token
+ * was sent to gives its gradient back, plus what reaches the token on other
+ * paths (its shared expert, the residual):
+ *
+ *   grad_x[t, :] = bf16( sum_j grad_expand_x[slot(t,j), :] + grad_x_add[t, :] )
+ *
+ * in fp32 over j ascending, then grad_x_add, then one round to nearest even.
+ * Dropped pairs contribute nothing; a token with none left gets grad_x_add,
+ * or 0.  (e4m3 dispatch: the quantisation counts as the identity.)
+ *
+ *  grad_expand_x  in  bf16 [capacity_rows, hidden].
+ *  grad_x_add     in  bf16 [bs, hidden], row stride grad_x_add_stride, or NULL;
+ *                     must not overlap grad_x (grad_x itself is refused).
+ *  grad_x         out bf16 [bs, hidden], contiguous.
+ *  other arguments as for moe_combine.
+ */
+int moe_dispatch_backward(const void* grad_expand_x, int64_t grad_expand_x_stride,
+                          int64_t capacity_rows, const int32_t* expert_ids,
+                          const int32_t* expand_idx, const int32_t* ep_send_counts,
+                          const void* grad_x_add, int64_t grad_x_add_stride, int32_t bs,
+                          int32_t hidden, int32_t k, int32_t num_experts, void* grad_x,
+                          int32_t* status, void* stream);
+
+/*
  * Compensation planner (host code, host pointers; no GPU involved).  The
  * DeepEP compensation PR (Python section) describes a water-filling
  * chunk-migration planner with expert-affinity batching, a makespan guard, a
