@@ -13,21 +13,20 @@
 // channels of ONE row, so the row's scale is one register per lane, the
 // weights' scale is the same for the whole wave, and the output leaves in
 // 8-byte stores.
+#include <type_traits>
+
 #include "moe_internal.h"
 
 namespace moe {
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kScaleBlock = 128;  // channels per scale
-constexpr int kTileThreads = 256;
-constexpr int kTileRows = 64;
-constexpr int kTileCols = 128;    // output channels per workgroup
 
 // The row tiles of all experts, from the device's counts: first[e] is the
 // number of tiles before expert e, first[E] their total.  Sums saturate at
@@ -35,9 +34,10 @@ constexpr int kTileCols = 128;    // output channels per workgroup
 // whose segments overlap cannot wrap them; such counts give no tiles at all.
 constexpr int kMostTiles = 1 << 30;
 
+template <int THREADS>
 struct TileMap {
   int first[kMaxExperts + 1];
-  int wave_sum[kTileThreads / kWave];
+  int wave_sum[THREADS / kWave];
 };
 
 // Rows of expert e that lie inside the buffer: [start, start + rows).
@@ -56,10 +56,11 @@ __device__ __forceinline__ void segment_of(const int32_t* __restrict__ counts,
   rows = (s < 0 || c <= 0 || s >= cap) ? 0 : (c < cap - s ? c : cap - s);
 }
 
-__device__ __forceinline__ void build_tile_map(TileMap& map, const int32_t* __restrict__ counts,
+template <int THREADS>
+__device__ __forceinline__ void build_tile_map(TileMap<THREADS>& map, const int32_t* __restrict__ counts,
                                                const int32_t* __restrict__ send, int32_t E,
                                                int64_t cap, int tile_rows, int32_t* status) {
-  constexpr int kPer = kMaxExperts / kTileThreads;
+  constexpr int kPer = kMaxExperts / THREADS;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   int n[kPer], sum = 0;
 #pragma unroll
@@ -85,7 +86,7 @@ __device__ __forceinline__ void build_tile_map(TileMap& map, const int32_t* __re
   __syncthreads();
   int base = incl - sum, total = 0;
 #pragma unroll
-  for (int w = 0; w < kTileThreads / kWave; ++w) {
+  for (int w = 0; w < THREADS / kWave; ++w) {
     if (w < wave) base = min(base + map.wave_sum[w], kMostTiles);
     total = min(total + map.wave_sum[w], kMostTiles);
   }
@@ -99,19 +100,6 @@ __device__ __forceinline__ void build_tile_map(TileMap& map, const int32_t* __re
   }
   if (tid == 0) map.first[E] = overlap ? 0 : total;
   __syncthreads();
-}
-
-// The expert whose tiles hold tile t (first[e] <= t < first[e + 1]).
-__device__ __forceinline__ int expert_of(const TileMap& map, int32_t E, int t) {
-  int lo = 0, hi = E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (map.first[mid + 1] > t)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  return lo;
 }
 
 struct ProductArgs {
@@ -131,55 +119,73 @@ struct ProductArgs {
   int32_t* status;
 };
 
-// Element offset in a 128-byte-row LDS tile, 16-byte chunks permuted by row
-// so that the 16 rows a fragment read touches fall on different banks.
-__device__ __forceinline__ int lds_chunk(int row, int chunk) {
-  return row * kScaleBlock + ((chunk ^ (row & 7)) << 4);
+// ---- pieces of a tile ----------------------------------------------------------
+// A tile's operands lie in shared memory as rows of 128 codes (one scale
+// block).  The 16-byte chunks of row r are permuted by (r / 2) % 8, so that
+// the 16 rows read together fall on all 64 banks once.
+__device__ __forceinline__ int chunk_slot(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+
+// 64 codes of a row: the lane's half of a block (chunks half, half + 2, ...;
+// both operands split a block alike, and the order inside a sum is free).
+struct Codes {
+  u32x4 c[4];
+};
+
+__device__ __forceinline__ Codes read_codes(const uint8_t* tile, int row, int half) {
+  Codes f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f.c[i] = *reinterpret_cast<const u32x4*>(tile + row * kScaleBlock +
+                                             (chunk_slot(row, 2 * i + half) << 4));
+  return f;
 }
 
-__device__ __forceinline__ i32x8 read_fragment(const uint8_t* tile, int row, int quarter) {
-  const u32x4 lo = *reinterpret_cast<const u32x4*>(tile + lds_chunk(row, quarter));
-  const u32x4 hi = *reinterpret_cast<const u32x4*>(tile + lds_chunk(row, quarter + 4));
-  i32x8 f;
+// The same codes as fp16 (exact), for sums in full fp32.
+struct Halves {
+  f16x8 h[8];
+};
+
+__device__ __forceinline__ f16x8 widen8(uint32_t lo, uint32_t hi) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.0f, false);
+  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.0f, true);
+  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.0f, false);
+  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.0f, true);
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+__device__ __forceinline__ Halves widen(const Codes& f) {
+  Halves w;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[i] = (int)lo[i];
-    f[4 + i] = (int)hi[i];
+    w.h[2 * i] = widen8(f.c[i][0], f.c[i][1]);
+    w.h[2 * i + 1] = widen8(f.c[i][2], f.c[i][3]);
   }
-  return f;
+  return w;
 }
 
-// The sum of a block's products from the e4m3 matrix instruction.  It adds
-// groups of 8 products aligned to the largest of them, of which it keeps 13
-// bits below the leading one; groups and blocks add up in fp32.
-__device__ __forceinline__ f32x4 block_product(const i32x8& w, const i32x8& x) {
-  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, 0, 0, 0, 0, 0, 0);
-}
-
-// Eight codes as fp16 (exact).
-__device__ __forceinline__ f16x8 widen8(int lo, int hi) {
-  f16x8 f;
+// The sum of a block's products, 32 weight rows x 32 token rows, from the
+// e4m3 matrix instruction.  It adds groups of 8 products aligned to the
+// largest of them, of which it keeps 13 bits below the leading one; groups
+// and blocks add up in fp32.
+__device__ __forceinline__ f32x16 block_product(const Codes& w, const Codes& x) {
+  f32x16 c = {};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(i ? hi : lo, 1.0f, false);
-    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(i ? hi : lo, 1.0f, true);
-    f[4 * i] = a[0];
-    f[4 * i + 1] = a[1];
-    f[4 * i + 2] = b[0];
-    f[4 * i + 3] = b[1];
+  for (int i = 0; i < 4; i += 2) {
+    const i32x8 a = {(int)w.c[i][0],     (int)w.c[i][1],     (int)w.c[i][2],     (int)w.c[i][3],
+                     (int)w.c[i + 1][0], (int)w.c[i + 1][1], (int)w.c[i + 1][2], (int)w.c[i + 1][3]};
+    const i32x8 b = {(int)x.c[i][0],     (int)x.c[i][1],     (int)x.c[i][2],     (int)x.c[i][3],
+                     (int)x.c[i + 1][0], (int)x.c[i + 1][1], (int)x.c[i + 1][2], (int)x.c[i + 1][3]};
+    c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
   }
-  return f;
+  return c;
 }
 
-// The same sum in full fp32: the codes widened to fp16, whose products the
-// matrix unit adds with 24 bits.
-__device__ __forceinline__ f32x4 block_product_fp32(const i32x8& w, const i32x8& x) {
-  f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+// The same sum with 24 bits throughout: the codes widened to fp16.
+__device__ __forceinline__ f32x16 block_product(const Halves& w, const Halves& x) {
+  f32x16 c = {};
 #pragma unroll
-  for (int i = 0; i < 8; i += 2)
-    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(w[i], w[i + 1]), widen8(x[i], x[i + 1]), c,
-                                               0, 0, 0);
+  for (int i = 0; i < 8; ++i)
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(w.h[i], x.h[i], c, 0, 0, 0);
   return c;
 }
 
@@ -191,180 +197,363 @@ __device__ __forceinline__ float gated(float g, float u) {
 
 // Four e4m3 codes of h / s (s = amax / 448).  A zero scale gives zero codes;
 // a block with an infinity or a NaN (its scale says so) gives NaN codes.
-__device__ __forceinline__ uint32_t codes4(const float (&h)[4], float s) {
+__device__ __forceinline__ uint32_t codes4(float h0, float h1, float h2, float h3, float s) {
   if (s == 0.0f) return 0u;
   if (!(s < __builtin_inff())) return 0x7F7F7F7Fu;
-  float q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_fmed3f(h[i] / s, 448.0f, -448.0f);
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
+  const float q0 = __builtin_amdgcn_fmed3f(h0 / s, 448.0f, -448.0f);
+  const float q1 = __builtin_amdgcn_fmed3f(h1 / s, 448.0f, -448.0f);
+  const float q2 = __builtin_amdgcn_fmed3f(h2 / s, 448.0f, -448.0f);
+  const float q3 = __builtin_amdgcn_fmed3f(h3 / s, 448.0f, -448.0f);
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(q0, q1, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(q2, q3, w, true);
   return (uint32_t)w;
 }
 
-template <bool GATED>
-__global__ __launch_bounds__(kTileThreads) void product_kernel(const ProductArgs p) {
-  constexpr int kSub = GATED ? 4 : 2;       // 16-channel weight tiles per wave
-  constexpr int kWRows = GATED ? 2 * kTileCols : kTileCols;
-  constexpr int kRowSub = kTileRows / 16;
-  constexpr int kXLoads = kTileRows * kScaleBlock / 16 / kTileThreads;
-  constexpr int kWLoads = kWRows * kScaleBlock / 16 / kTileThreads;
-  __shared__ TileMap map;
-  __shared__ alignas(16) uint8_t x_lds[kTileRows * kScaleBlock];
-  __shared__ alignas(16) uint8_t w_lds[kWRows * kScaleBlock];
-  __shared__ uint32_t amax_lds[kTileThreads / kWave][kTileRows];
+// ---- asynchronous loads into shared memory ---------------------------------------
+// 64 lanes' 16 (or 4) bytes go to 64 consecutive places from lds_base on,
+// each lane from its own address.  The loads have no destination registers;
+// wait_and_meet counts them.  (As builtins the compiler would wait for the
+// newest of them before every read of shared memory.)  M0 is the loads' own:
+// nothing else in these kernels uses it.
+__device__ __forceinline__ void load_lds16(uint32_t lds_base, uint32_t offset, const void* base) {
+  __asm__ volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(lds_base), "v"(offset), "s"(base)
+      : "memory");
+}
 
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  const int l16 = lane & 15, quarter = lane >> 4;
+__device__ __forceinline__ void load_lds4(uint32_t lds_base, const void* addr) {
+  __asm__ volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, off"
+      :
+      : "s"(lds_base), "v"(addr)
+      : "memory");
+}
+
+// Waits until at most LEFT of this wave's memory operations are in flight
+// and its reads of shared memory are done, then for the whole workgroup.
+template <int LEFT>
+__device__ __forceinline__ void wait_and_meet() {
+  __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(LEFT) : "memory");
+}
+
+// The workgroup meets; only shared memory is waited for.
+__device__ __forceinline__ void meet() {
+  __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v);
+  const int hi = uniform((int)(v >> 32));
+  return ((int64_t)hi << 32) | lo;
+}
+
+// ---- the kernel -------------------------------------------------------------------
+// Workgroups of WR x WC waves; each wave holds RT x CT sums of 32 token rows
+// x 32 weight rows.  Gated, half of a wave's weight rows are gate rows and
+// half the up rows of the same channels.
+template <bool GATED_, int RT_, int CT_, int WR_, int WC_, int STAGES_>
+struct Shape {
+  static constexpr bool kGated = GATED_;
+  static constexpr int RT = RT_, CT = CT_, WR = WR_, WC = WC_, kStages = STAGES_;
+  static constexpr int kWaves = WR * WC;
+  static constexpr int kThreads = kWaves * kWave;
+  static constexpr int kRows = WR * RT * 32;
+  static constexpr int kWRows = WC * CT * 32;
+  static constexpr int kCols = kGated ? kWRows / 2 : kWRows;   // output channels
+  static constexpr int kWBlocks = kWRows / kScaleBlock;        // weight scales a step
+  static constexpr int kXLoads = kRows / 8 / kWaves;           // 16-byte loads a wave and step
+  static constexpr int kWLoads = kWRows / 8 / kWaves;
+  static constexpr int kLoads = kXLoads + kWLoads + 1;
+  static constexpr int kScaleSlots = (kRows + kWBlocks + kWave - 1) / kWave * kWave;
+  static constexpr int kXBytes = kRows * kScaleBlock;
+  static constexpr int kWBytes = kWRows * kScaleBlock;
+  static constexpr int kStageBytes = kXBytes + kWBytes + kScaleSlots * 4;
+  static_assert(kXLoads * 8 * kWaves == kRows && kWLoads * 8 * kWaves == kWRows, "whole loads");
+  static_assert(!kGated || (kCols == kScaleBlock && CT % 2 == 0), "one scale block a tile");
+  static_assert((kGated ? CT / 2 : CT) * 32 <= kScaleBlock, "a wave's channels share a scale");
+  static_assert((kStages - 2) * kLoads < 64, "the wait counts to 63");
+};
+
+// Where a tile lies.
+struct TileAt {
+  int64_t row0;   // its first row
+  int32_t live;   // its rows
+  int32_t e, ct;  // expert, column tile
+};
+
+constexpr int kRowGroup = 8;  // row tiles that walk the columns together
+
+template <class S>
+__device__ __forceinline__ TileAt locate(const ProductArgs& p, const TileMap<S::kThreads>& map,
+                                         int64_t tile, int32_t col_tiles) {
+  const int64_t t = (tile >> 31) ? tile / col_tiles : (int64_t)((uint32_t)tile / (uint32_t)col_tiles);
+  // The number of experts whose tiles end at or before t.
+  const int lane = threadIdx.x & (kWave - 1);
+  int e = 0;
+  for (int i = 0; i < p.E; i += kWave) {
+    const bool before = i + lane < p.E && map.first[i + lane + 1] <= t;
+    const int n = __popcll(__ballot(before));
+    e += n;
+    if (n < kWave) break;
+  }
+  e = uniform(e);
+  const int32_t first = uniform(map.first[e]);
+  const int32_t row_tiles = uniform(map.first[e + 1]) - first;
+  // Groups of row tiles, inside a group column by column.
+  const int64_t in_expert = tile - (int64_t)first * col_tiles;
+  const int64_t group_tiles = (int64_t)kRowGroup * col_tiles;
+  const int32_t group = (int32_t)(in_expert >> 31 ? in_expert / group_tiles
+                                                  : (uint32_t)in_expert / (uint32_t)group_tiles);
+  const uint32_t in_group = (uint32_t)(in_expert - group * group_tiles);
+  const uint32_t wide = (uint32_t)min(kRowGroup, row_tiles - group * kRowGroup);
+  TileAt at;
+  at.e = e;
+  at.ct = uniform((int)(in_group / wide));
+  const int32_t rt = group * kRowGroup + (int32_t)(in_group % wide);
+  int64_t start, rows;
+  bool cut;
+  segment_of(p.counts, p.send, p.cap, e, start, rows, cut);
+  at.row0 = uniform64(start + (int64_t)rt * S::kRows);
+  at.live = uniform((int)min((int64_t)S::kRows, start + rows - at.row0));
+  return at;
+}
+
+template <class S>
+__global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs p) {
+  constexpr bool kGated = S::kGated;
+  constexpr int RT = S::RT, CT = S::CT, kStages = S::kStages;
+  using Operand = std::conditional_t<kGated, Halves, Codes>;
+  __shared__ alignas(1024) uint8_t ring[kStages * S::kStageBytes];
+  __shared__ TileMap<S::kThreads> map;
+  __shared__ uint32_t amax_lds[kGated ? S::WC : 1][S::kRows];
+
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid / kWave);
+  const int l32 = lane & 31, half = lane >> 5;
+  const int wr = wave / S::WC, wc = wave % S::WC;
   const int32_t kb = p.K / kScaleBlock, nb = (p.N + kScaleBlock - 1) / kScaleBlock;
-  const int32_t col_tiles = (p.cols + kTileCols - 1) / kTileCols;
-  build_tile_map(map, p.counts, p.send, p.E, p.cap, kTileRows, p.status);
-  const int64_t tiles = (int64_t)map.first[p.E] * col_tiles;
+  const int32_t col_tiles = (p.cols + S::kCols - 1) / S::kCols;
+  build_tile_map<S::kThreads>(map, p.counts, p.send, p.E, p.cap, S::kRows, p.status);
+  const int64_t tiles = (int64_t)uniform(map.first[p.E]) * col_tiles;
 
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int e = expert_of(map, p.E, (int)(tile / col_tiles));
-    const int32_t row_tiles = map.first[e + 1] - map.first[e];
-    const int64_t in_expert = tile - (int64_t)map.first[e] * col_tiles;
-    const int32_t ct = (int32_t)(in_expert / row_tiles), rt = (int32_t)(in_expert % row_tiles);
-    int64_t start, rows;
-    bool cut;
-    segment_of(p.counts, p.send, p.cap, e, start, rows, cut);
-    const int64_t row0 = start + (int64_t)rt * kTileRows;
-    const int32_t live = (int32_t)min((int64_t)kTileRows, start + rows - row0);
-    const int32_t col0 = ct * kTileCols;
-    const uint8_t* we = p.w + (int64_t)e * p.N * p.K;
-    const float* wse = p.w_scales + (int64_t)e * nb * kb;
+  // Workgroups i, i + 8, ... share an XCD's L2: give each XCD neighbouring tiles.
+  const int per_xcd = gridDim.x / 8;
+  const int first_tile = gridDim.x % 8 == 0 ? (blockIdx.x % 8) * per_xcd + blockIdx.x / 8
+                                            : blockIdx.x;
+  const uint32_t ring_base = (uint32_t)(uintptr_t)ring;
 
-    const uint8_t* x_src[kXLoads];
-    const uint8_t* w_src[kWLoads];
-    int x_dst[kXLoads], w_dst[kWLoads];
+  // The loads' side: its tile and block, and each lane's offsets in the tile.
+  int64_t load_tile = first_tile;
+  int32_t load_b = 0;
+  int load_stage = 0;
+  uint32_t x_off[S::kXLoads], w_off[S::kWLoads];
+  const uint8_t *x_base = nullptr, *w_base = nullptr;
+  const float* scale_src = nullptr;
+
+  auto begin_loads = [&]() {
+    const TileAt at = locate<S>(p, map, load_tile, col_tiles);
 #pragma unroll
-    for (int i = 0; i < kXLoads; ++i) {
-      const int c = i * kTileThreads + tid, row = c >> 3;
-      x_src[i] = p.x + (row0 + min(row, live - 1)) * p.xs + (c & 7) * 16;
-      x_dst[i] = lds_chunk(row, c & 7);
+    for (int i = 0; i < S::kXLoads; ++i) {
+      const int row = (wave * S::kXLoads + i) * 8 + (lane >> 3);
+      x_off[i] = (uint32_t)(min(row, at.live - 1) * p.xs) +
+                 ((uint32_t)chunk_slot(row, lane & 7) << 4);
     }
+    // A wave's weight loads lie in one half of the tile (gate or up rows).
+    const int w_row0 = wave * S::kWLoads * 8;
+    const bool up = kGated && w_row0 >= S::kCols;
+    const int32_t col0 = at.ct * S::kCols;
 #pragma unroll
-    for (int i = 0; i < kWLoads; ++i) {
-      const int c = i * kTileThreads + tid, row = c >> 3;
-      const int in_half = row & (kTileCols - 1);
-      const int64_t n = min(col0 + in_half, p.cols - 1) + (row >= kTileCols ? p.cols : 0);
-      w_src[i] = we + n * p.K + (c & 7) * 16;
-      w_dst[i] = lds_chunk(row, c & 7);
+    for (int i = 0; i < S::kWLoads; ++i) {
+      const int row = w_row0 + i * 8 + (lane >> 3);
+      const int in_half = up ? row - S::kCols : row;
+      w_off[i] = (uint32_t)min(in_half, p.cols - 1 - col0) * (uint32_t)p.K +
+                 ((uint32_t)chunk_slot(row, lane & 7) << 4);
     }
-    const float* xs_src[kRowSub];
+    x_base = p.x + at.row0 * p.xs;
+    w_base = p.w + ((int64_t)at.e * p.N + col0 + (up ? p.cols : 0)) * p.K;
+    const int i = (wave % (S::kScaleSlots / kWave)) * kWave + lane;
+    const float* xs = p.x_scales + (at.row0 + min(i, at.live - 1)) * kb;
+    const int32_t block = kGated ? at.ct + (i > S::kRows ? p.cols / kScaleBlock : 0)
+                                 : min(at.ct * S::kWBlocks + max(i - S::kRows, 0), nb - 1);
+    const float* ws = p.w_scales + ((int64_t)at.e * nb + min(block, nb - 1)) * kb;
+    scale_src = i < S::kRows ? xs : ws;
+  };
+  auto issue_loads = [&]() {
+    const uint32_t stage = ring_base + load_stage * S::kStageBytes;
+    const int64_t at = (int64_t)load_b * kScaleBlock;
 #pragma unroll
-    for (int r = 0; r < kRowSub; ++r)
-      xs_src[r] = p.x_scales + (row0 + min(r * 16 + l16, live - 1)) * kb;
-    const float* ws_src[GATED ? 2 : 1];
-    ws_src[0] = wse + (int64_t)(col0 / kScaleBlock) * kb;
-    if (GATED) ws_src[GATED ? 1 : 0] = wse + (int64_t)((p.cols + col0) / kScaleBlock) * kb;
+    for (int i = 0; i < S::kXLoads; ++i)
+      load_lds16(stage + (wave * S::kXLoads + i) * 1024, x_off[i], x_base + at);
+#pragma unroll
+    for (int i = 0; i < S::kWLoads; ++i)
+      load_lds16(stage + S::kXBytes + (wave * S::kWLoads + i) * 1024, w_off[i], w_base + at);
+    load_lds4(stage + S::kXBytes + S::kWBytes +
+                  (wave % (S::kScaleSlots / kWave)) * (kWave * 4),
+              scale_src + load_b);
+    load_stage = load_stage + 1 == kStages ? 0 : load_stage + 1;
+    if (++load_b == kb) {
+      load_b = 0;
+      load_tile += gridDim.x;
+      if (load_tile < tiles) begin_loads();
+    }
+  };
 
-    f32x4 acc[kSub][kRowSub];
+  if (load_tile < tiles) begin_loads();
 #pragma unroll
-    for (int s = 0; s < kSub; ++s)
+  for (int s = 0; s < kStages - 1; ++s)
+    if (load_tile < tiles) issue_loads();
+
+  int stage = 0;
+  for (int64_t tile = first_tile; tile < tiles; tile += gridDim.x) {
+    f32x16 acc[CT][RT];
 #pragma unroll
-      for (int r = 0; r < kRowSub; ++r) acc[s][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[c][r] = f32x16{};
 
     for (int32_t b = 0; b < kb; ++b) {
-      u32x4 xv[kXLoads], wv[kWLoads];
+      // This stage's loads are done, everyone's, and the stage before it is
+      // read: its place takes the next loads.
+      if (load_tile < tiles) {
+        wait_and_meet<(kStages - 2) * S::kLoads>();
+        issue_loads();
+      } else {
+        wait_and_meet<0>();
+      }
+      const uint8_t* x_lds = ring + stage * S::kStageBytes;
+      const uint8_t* w_lds = x_lds + S::kXBytes;
+      const float* scales = reinterpret_cast<const float*>(w_lds + S::kWBytes);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+
+      Operand xf[RT];
+      float sx[RT];
 #pragma unroll
-      for (int i = 0; i < kXLoads; ++i)
-        xv[i] = *reinterpret_cast<const u32x4*>(x_src[i] + (int64_t)b * kScaleBlock);
+      for (int r = 0; r < RT; ++r) {
+        const int row = (wr * RT + r) * 32 + l32;
+        const Codes codes = read_codes(x_lds, row, half);
+        if constexpr (kGated)
+          xf[r] = widen(codes);
+        else
+          xf[r] = codes;
+        sx[r] = scales[row];
+      }
 #pragma unroll
-      for (int i = 0; i < kWLoads; ++i)
-        wv[i] = *reinterpret_cast<const u32x4*>(w_src[i] + (int64_t)b * kScaleBlock);
-      float sx[kRowSub];
+      for (int c = 0; c < CT; ++c) {
+        const bool up = kGated && c >= CT / 2;
+        const int w_row = kGated ? (up ? S::kCols : 0) + (wc * (CT / 2) + (up ? c - CT / 2 : c)) * 32
+                                 : (wc * CT + c) * 32;
+        const Codes codes = read_codes(w_lds, w_row + l32, half);
+        const float sw = scales[S::kRows + (kGated ? (up ? 1 : 0) : w_row / kScaleBlock)];
+        Operand wf;
+        if constexpr (kGated)
+          wf = widen(codes);
+        else
+          wf = codes;
 #pragma unroll
-      for (int r = 0; r < kRowSub; ++r) sx[r] = xs_src[r][b];
-      __syncthreads();  // the previous block's fragments are read
-#pragma unroll
-      for (int i = 0; i < kXLoads; ++i) *reinterpret_cast<u32x4*>(x_lds + x_dst[i]) = xv[i];
-#pragma unroll
-      for (int i = 0; i < kWLoads; ++i) *reinterpret_cast<u32x4*>(w_lds + w_dst[i]) = wv[i];
-      __syncthreads();
-      i32x8 xf[kRowSub];
-#pragma unroll
-      for (int r = 0; r < kRowSub; ++r) xf[r] = read_fragment(x_lds, r * 16 + l16, quarter);
-#pragma unroll
-      for (int s = 0; s < kSub; ++s) {
-        const int row = (s >> 1) * kTileCols + wave * 32 + (s & 1) * 16 + l16;
-        const i32x8 wf = read_fragment(w_lds, row, quarter);
-        const float sw = ws_src[GATED ? s >> 1 : 0][b];
-#pragma unroll
-        for (int r = 0; r < kRowSub; ++r) {
-          const f32x4 part = GATED ? block_product_fp32(wf, xf[r]) : block_product(wf, xf[r]);
+        for (int r = 0; r < RT; ++r) {
+          const f32x16 part = block_product(wf, xf[r]);
           const float f = sx[r] * sw;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[s][r][i] = __builtin_fmaf(f, part[i], acc[s][r][i]);
+          for (int i = 0; i < 16; ++i) acc[c][r][i] = __builtin_fmaf(f, part[i], acc[c][r][i]);
         }
       }
     }
 
-    if constexpr (!GATED) {
+    // A lane holds, of each sum, row l32 and channels 8 q + 4 half + 0..3.
+    const TileAt at = locate<S>(p, map, tile, col_tiles);
+    const int32_t col0 = at.ct * S::kCols;
+    if constexpr (!kGated) {
 #pragma unroll
-      for (int r = 0; r < kRowSub; ++r) {
-        const int row = r * 16 + l16;
-        if (row >= live) continue;
+      for (int r = 0; r < RT; ++r) {
+        const int row = (wr * RT + r) * 32 + l32;
+        if (row >= at.live) continue;
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + (at.row0 + row) * p.out_stride;
 #pragma unroll
-        for (int s = 0; s < kSub; ++s) {
-          const int32_t col = col0 + wave * 32 + s * 16 + quarter * 4;
+        for (int c = 0; c < CT; ++c) {
+          const int32_t col = col0 + (wc * CT + c) * 32;
           if (col >= p.cols) continue;
-          const f32x4 v = acc[s][r];
-          const u32x2 o = {f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
-                           f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16)};
-          *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.out) + (row0 + row) * p.out_stride +
-                                    col) = o;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16& v = acc[c][r];
+            const u32x2 o = {
+                f32_to_bf16_rne(v[4 * q]) | (f32_to_bf16_rne(v[4 * q + 1]) << 16),
+                f32_to_bf16_rne(v[4 * q + 2]) | (f32_to_bf16_rne(v[4 * q + 3]) << 16)};
+            *reinterpret_cast<u32x2*>(dst + col + 8 * q + 4 * half) = o;
+          }
         }
       }
     } else {
-      float h[2][kRowSub][4];
+      constexpr int CH = CT / 2;
 #pragma unroll
-      for (int r = 0; r < kRowSub; ++r) {
+      for (int r = 0; r < RT; ++r) {
         uint32_t m = 0;
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            h[s][r][i] = gated(acc[s][r][i], acc[(GATED ? 2 : 0) + s][r][i]);
-            m = max(m, __float_as_uint(h[s][r][i]) & 0x7FFFFFFFu);
+          for (int i = 0; i < 16; ++i) {
+            acc[c][r][i] = gated(acc[c][r][i], acc[CT / 2 + c][r][i]);
+            m = max(m, __float_as_uint(acc[c][r][i]) & 0x7FFFFFFFu);
           }
-        m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
         m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
-        if (quarter == 0) amax_lds[wave][r * 16 + l16] = m;
+        if (half == 0) amax_lds[wc][(wr * RT + r) * 32 + l32] = m;
       }
-      __syncthreads();
+      meet();
 #pragma unroll
-      for (int r = 0; r < kRowSub; ++r) {
-        const int row = r * 16 + l16;
+      for (int r = 0; r < RT; ++r) {
+        const int row = (wr * RT + r) * 32 + l32;
         uint32_t m = 0;
 #pragma unroll
-        for (int w = 0; w < kTileThreads / kWave; ++w) m = max(m, amax_lds[w][row]);
+        for (int w = 0; w < S::WC; ++w) m = max(m, amax_lds[w][row]);
         const float s = __uint_as_float(m) / 448.0f;
-        if (row < live) {
+        if (row >= at.live) continue;
+        uint8_t* dst = static_cast<uint8_t*>(p.out) + (at.row0 + row) * p.out_stride + col0;
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) +
-                                         (row0 + row) * p.out_stride + col0 + wave * 32 +
-                                         i * 16 + quarter * 4) = codes4(h[i][r], s);
-          if (wave == 0 && quarter == 0)
-            p.out_scales[(row0 + row) * (p.cols / kScaleBlock) + ct] = s;
+        for (int c = 0; c < CH; ++c) {
+          const f32x16& v = acc[c][r];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint32_t*>(dst + (wc * CH + c) * 32 + 8 * q + 4 * half) =
+                codes4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3], s);
         }
+        if (wc == 0 && half == 0)
+          p.out_scales[(at.row0 + row) * (p.cols / kScaleBlock) + at.ct] = s;
       }
-      __syncthreads();  // amax_lds is free for the next tile
+      meet();  // amax_lds is free for the next tile
     }
   }
 }
 
+constexpr int kComputeUnits = 256;
+
+template <class S>
+hipError_t launch_shape(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
+  const int64_t col_tiles = (p.cols + S::kCols - 1) / S::kCols;
+  const int64_t row_tiles =
+      expected_rows / S::kRows + (p.counts ? (expected_rows < p.E ? expected_rows : p.E) : 1);
+  constexpr int kPerUnit = 160 * 1024 / (S::kStages * S::kStageBytes + 4096);
+  const int64_t most = kComputeUnits * (kPerUnit < 1 ? 1 : kPerUnit);
+  const int64_t want = row_tiles * col_tiles;
+  const dim3 grid((uint32_t)(want < 1 ? 1 : want < most ? want : most));
+  launch_kernel(product_kernel<S>, grid, S::kThreads, stream, p);
+  return hipGetLastError();
+}
+
 template <bool GATED>
 hipError_t launch_product(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
-  const int64_t col_tiles = (p.cols + kTileCols - 1) / kTileCols;
-  const int64_t row_tiles =
-      expected_rows / kTileRows + (p.counts ? (expected_rows < p.E ? expected_rows : p.E) : 1);
-  const int64_t want = row_tiles * col_tiles;
-  const dim3 grid((uint32_t)(want < 1 ? 1 : want < 65536 ? want : 65536));
-  launch_kernel(product_kernel<GATED>, grid, kTileThreads, stream, p);
-  return hipGetLastError();
+  const int64_t per_expert = expected_rows / p.E;
+  if constexpr (GATED) {
+    if (per_expert <= 32) return launch_shape<Shape<true, 1, 2, 1, 4, 4>>(p, expected_rows, stream);
+    return launch_shape<Shape<true, 2, 2, 2, 4, 3>>(p, expected_rows, stream);
+  } else {
+    if (per_expert <= 32) return launch_shape<Shape<false, 1, 1, 1, 4, 3>>(p, expected_rows, stream);
+    return launch_shape<Shape<false, 2, 2, 2, 4, 3>>(p, expected_rows, stream);
+  }
 }
 
 }  // namespace

@@ -463,6 +463,8 @@ struct GroupedGemm {
   float* out_scales = nullptr;        // [capacity_rows, out_features / 128] with `gated`
   int32_t* status = nullptr;
 };
+// Row offsets inside a tile of at most 256 rows are 32-bit.
+constexpr int64_t kMaxProductStride = int64_t(1) << 23;
 hipError_t launch_grouped_gemm(const GroupedGemm& g, hipStream_t stream);
 
 }  // namespace moe

@@ -437,7 +437,8 @@ int moe_dispatch_fused_replicated(const void* x, int64_t x_stride, int32_t bs, i
  *
  *  expand_x       in  e4m3fn codes [capacity_rows, in_features], row stride
  *                     expand_x_stride bytes (>= in_features, a multiple of
- *                     16), 16-byte aligned: moe_dispatch's e4m3 output.
+ *                     16, at most 2^23), 16-byte aligned: moe_dispatch's
+ *                     e4m3 output.
  *  capacity_rows  in  rows of expand_x and out, >= 0, at most 2^30.
  *  quant_scales   in  fp32 [capacity_rows, in_features/128] row-major.
  *  weight         in  e4m3fn codes [num_experts, out_features, in_features],
