@@ -153,6 +153,8 @@ int product_call(const moe::GroupedGemm& g, void* stream) {
     return MOE_ERR_INVALID_ARG;
   if (g.capacity_rows < 0 || g.capacity_rows > moe::kMaxRows || g.expected_rows < 0)
     return MOE_ERR_INVALID_ARG;
+  // Tiles are counted in 32 bits.
+  if (g.capacity_rows > (int64_t(1) << 40) / g.out_features) return MOE_ERR_INVALID_ARG;
   if (g.capacity_rows == 0) return MOE_OK;
   if (!row_ok(g.x, g.x_stride, g.in_features, 1)) return MOE_ERR_INVALID_ARG;
   if (g.x_stride > moe::kMaxProductStride) return MOE_ERR_INVALID_ARG;
