@@ -27,8 +27,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-#define MOE_INLINE __attribute__((always_inline))
-
 constexpr int kScaleBlock = 128;  // channels per scale
 
 // Rows of expert e that lie inside the buffer: [start, start + rows).
@@ -148,38 +146,34 @@ struct Codes {
 };
 
 template <bool WIDE>
-__device__ __forceinline__ void read_chunk(Codes<WIDE>& f, int i, const uint8_t* tile, int row,
-                                           int key, int group) {
-  f.c[i] = *reinterpret_cast<const u32x4*>(
-      tile + row * kScaleBlock + (((i * Unit<WIDE>::kGroups + group) ^ key) << 4));
-}
-
-template <bool WIDE>
 __device__ __forceinline__ void read_codes(Codes<WIDE>& f, const uint8_t* tile, int row, int key,
                                            int group) {
 #pragma unroll
-  for (int i = 0; i < Unit<WIDE>::kChunks; ++i) read_chunk(f, i, tile, row, key, group);
+  for (int i = 0; i < Unit<WIDE>::kChunks; ++i)
+    f.c[i] = *reinterpret_cast<const u32x4*>(
+        tile + row * kScaleBlock + (((i * Unit<WIDE>::kGroups + group) ^ key) << 4));
 }
 
-// The codes as fp16 (exact): the fp16 instruction adds their products with 24
-// bits throughout, for sums in full fp32.
+// The codes as fp16 (exact), for sums in full fp32.
 struct Halves {
   f16x8 h[8];
 };
 
-__device__ __forceinline__ f16x8 widen8(const Codes<true>& f, int i) {
-  const int lo = (int)f.c[i / 2][i % 2 * 2], hi = (int)f.c[i / 2][i % 2 * 2 + 1];
-  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
-  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
-  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
-  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+__device__ __forceinline__ f16x8 widen8(uint32_t lo, uint32_t hi) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.0f, false);
+  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.0f, true);
+  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.0f, false);
+  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.0f, true);
   return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-__device__ __forceinline__ Halves widen(const Codes<true>& f) {
+__device__ __forceinline__ Halves as_operand(const Codes<true>& f) {
   Halves w;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w.h[i] = widen8(f, i);
+  for (int i = 0; i < 4; ++i) {
+    w.h[2 * i] = widen8(f.c[i][0], f.c[i][1]);
+    w.h[2 * i + 1] = widen8(f.c[i][2], f.c[i][3]);
+  }
   return w;
 }
 
@@ -193,6 +187,15 @@ __device__ __forceinline__ i32x8 as_operand(const Codes<false>& f) {
 // bits below the leading one; groups and blocks add up in fp32.
 __device__ __forceinline__ f32x4 block_product(const i32x8& w, const i32x8& x) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{}, 0, 0, 0, 0, 0, 0);
+}
+
+// The same sum with 24 bits throughout: the codes widened to fp16.
+__device__ __forceinline__ f32x16 block_product(const Halves& w, const Halves& x) {
+  f32x16 c = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(w.h[i], x.h[i], c, 0, 0, 0);
+  return c;
 }
 
 // sum += f * part, element by element.
@@ -230,35 +233,25 @@ __device__ __forceinline__ uint32_t codes4(float h0, float h1, float h2, float h
   return (uint32_t)w;
 }
 
-// f(0), f(1), .. f(N - 1), each with its number as a type.
-template <int N, int I = 0, class F>
-__device__ __forceinline__ void static_for(const F& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>{});
-    static_for<N, I + 1>(f);
-  }
-}
-
 // A value that is the same in every lane, in a scalar register.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // ---- asynchronous loads into shared memory ---------------------------------------
-// 64 lanes' 16 (or 4) bytes go to 64 consecutive places of shared memory,
+// 64 lanes' 16 (or 4) bytes go to 64 consecutive places from lds_base on,
 // each lane from its own address.  The loads have no destination registers;
 // wait_and_meet counts them.  (As builtins the compiler would wait for the
-// newest of them before every read of shared memory.)  M0 is the loads' own:
+// newest of them before every read of shared memory.)  The compiler does not
+// look inside: the five wait states that a scalar address needs after a
+// vector instruction (a readfirstlane) has written it are here.  M0 is the loads' own:
 // nothing else in these kernels uses it.
-// They are ordered among themselves and with the waits, not with reads of
-// shared memory: a block's place is not read between the two.  The compiler
-// does not look inside: the five wait states that a scalar address needs
-// after a vector instruction (a readfirstlane) has written it are here.
 __device__ __forceinline__ void load_lds16(uint32_t lds_base, uint32_t offset, const void* base) {
   __asm__ volatile(
       "s_mov_b32 m0, %0\n\t"
       "s_nop 4\n\t"
       "global_load_lds_dwordx4 %1, %2"
       :
-      : "s"(uniform((int)lds_base)), "v"(offset), "s"(base));
+      : "s"(uniform((int)lds_base)), "v"(offset), "s"(base)
+      : "memory");
 }
 
 __device__ __forceinline__ void load_lds4(uint32_t lds_base, const void* addr) {
@@ -267,7 +260,8 @@ __device__ __forceinline__ void load_lds4(uint32_t lds_base, const void* addr) {
       "s_nop 4\n\t"
       "global_load_lds_dword %1, off"
       :
-      : "s"(uniform((int)lds_base)), "v"(addr));
+      : "s"(uniform((int)lds_base)), "v"(addr)
+      : "memory");
 }
 
 // Waits until at most LEFT of this wave's memory operations are in flight
@@ -295,6 +289,9 @@ __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
 // ---- the kernel -------------------------------------------------------------------
 constexpr int kScaleSteps = 4;  // blocks whose scales are loaded together
 constexpr int kRowGroup = 8;    // row tiles that walk the columns together
+constexpr int kTurnStride = 4096;
+constexpr int kTurnCols = 256;  // channels whose sums begin at the same block
+constexpr int kTurnBlocks = 7;  // and how much further on the next ones do
 
 // Workgroups of WR x WC waves; each wave holds RT x CT squares of token rows x
 // weight rows.  Gated, half of a wave's weight rows are gate rows and half
@@ -315,7 +312,6 @@ struct Shape {
   static constexpr int kXLoads = kRows / 8 / kWaves;           // 16-byte loads a wave and step
   static constexpr int kWLoads = kWRows / 8 / kWaves;
   static constexpr int kLoads = kXLoads + kWLoads;
-  static constexpr int kLoadsAfterMeeting = 2 * kLoads / CT;   // of a step; the others before
   static constexpr int kXBytes = kRows * kScaleBlock;
   static constexpr int kWBytes = kWRows * kScaleBlock;
   static constexpr int kStageBytes = kXBytes + kWBytes;
@@ -341,11 +337,13 @@ struct Shape {
     return kGated ? (row >> 1 & 3) | (row >> 4 & 1) << 2 : (row >> 1 & 1) | (row >> 3 & 3) << 1;
   }
   static_assert(kRun % kPiece == 0, "whole stores");
-  // 16-byte stores of a wave and tile.
-  static constexpr int kStores = RT * kRun / kPiece;
-  static constexpr int kStoredWaits = kStages - 1 - (kLoadsAfterMeeting < kLoads ? 1 : 0);
-  static_assert(CT >= 2 && CT % 2 == 0 && (!kGated || RT == 1), "the order of a step");
-  static_assert((kStages - 1) * kLoads + kStores < 64, "the wait counts to 63");
+  static_assert(kTurnCols % kCols == 0, "a tile's sums begin at one block");
+  static_assert(kXLoads * 8 * kWaves == kRows && kWLoads * 8 * kWaves == kWRows, "whole loads");
+  static_assert(kRows % (kWave / kScaleSteps) == 0, "whole scale loads");
+  static_assert(!kGated || (kCols == kScaleBlock && CT % 2 == 0), "one scale block a tile");
+  static_assert(kScaleBlock % ((kGated ? CT / 2 : CT) * kSide) == 0,
+                "a wave's channels share a scale");
+  static_assert((kStages - 1) * kLoads < 64, "the wait counts to 63");
 };
 
 template <class S>
@@ -393,26 +391,27 @@ __device__ __forceinline__ TileAt locate(const ProductArgs& p, const TileMap<S::
   return at;
 }
 
-// One workgroup's loads: the blocks of its tiles, one after the other.
+// One workgroup's loads: a tile and a block in it, and what they have in
+// shared memory.
 template <class S>
 struct Loader {
   const ProductArgs& p;
   Shared<S>& sh;
   int32_t kb, nb;
-  uint32_t col_tiles;
+  uint32_t tiles, col_tiles;
   int lane, wave;
-  uint32_t tile;       // the tile the next block with b == 0 begins
-  int32_t left;        // blocks not sent for yet
+  uint32_t tile;
   int32_t b = 0;
-  int scale_at = 0;
-  uint32_t ring_at;    // the wave's place in a stage
+  int stage = 0, scale_at = 0;
   TileAt at = {};
   uint32_t x_off[S::kXLoads], w_off[S::kWLoads];
   const uint8_t *x_at = nullptr, *w_at = nullptr;
+  int32_t turn = 0;    // the block a tile begins with
+
+  __device__ __forceinline__ bool more() const { return tile < tiles; }
 
   __device__ __forceinline__ void begin_tile() {
     at = locate<S>(p, sh.map, tile, col_tiles);
-    tile += gridDim.x;
 #pragma unroll
     for (int i = 0; i < S::kXLoads; ++i) {
       const int row = (wave * S::kXLoads + i) * 8 + (lane >> 3);
@@ -430,15 +429,24 @@ struct Loader {
       w_off[i] = (uint32_t)min(in_half, p.cols - 1 - col0) * (uint32_t)p.K +
                  ((uint32_t)((lane & 7) ^ S::w_key(in_half)) << 4);
     }
-    x_at = uniform_ptr(p.x + at.row0 * p.xs);
-    w_at = uniform_ptr(p.w + ((int64_t)at.e * p.N + col0 + (up ? p.cols : 0)) * p.K);
+    // Weight rows a multiple of 4096 bytes apart share memory channels, and
+    // tiles that run together would all ask the same few: there column tiles
+    // begin at different blocks and go round (64 experts of 8 rows, 4096
+    // channels: 181 -> 151 us gated, 117 -> 96 us plain; elsewhere it costs
+    // up to 4 %, tiles side by side no longer sharing the rows they read).
+    // The start depends on the output channel alone, so the sums of a row do
+    // not depend on the tile's shape or the rows with it.
+    turn = p.K % kTurnStride == 0 ? col0 / kTurnCols * kTurnBlocks % kb : 0;
+    x_at = p.x + at.row0 * p.xs + turn * kScaleBlock;
+    w_at = p.w + ((int64_t)at.e * p.N + col0 + (up ? p.cols : 0)) * p.K + turn * kScaleBlock;
   }
 
   // The next kScaleSteps blocks' scales (4 lanes a row; past the last block
   // or row, the last one's again).
   __device__ __forceinline__ void issue_scales() {
     const uint32_t to = (uint32_t)(uintptr_t)sh.scales[scale_at];
-    const int32_t block = min(b + (lane & (kScaleSteps - 1)), kb - 1);
+    int32_t block = min(b + (lane & (kScaleSteps - 1)), kb - 1) + turn;
+    if (block >= kb) block -= kb;
     constexpr int kPer = kWave / kScaleSteps;
     for (int i = wave; i < S::kRows / kPer; i += S::kWaves) {
       const int row = i * kPer + lane / kScaleSteps;
@@ -455,41 +463,48 @@ struct Loader {
     scale_at = scale_at + 1 == S::kStages ? 0 : scale_at + 1;
   }
 
-  // Turns to the next block, whose scales' loads go off first.  Past the last
-  // block it stays there: its loads are sent again, into a place that nobody
-  // reads, so that every step has as many loads to count.
-  __device__ __forceinline__ void next_block() {
-    if (left == 0) return;
-    --left;
+  // Sends off the next block's loads, if there is one; its scales' first.
+  __device__ __forceinline__ void issue() {
+    if (!more()) return;
     if (b == 0) {
       begin_tile();
     } else {
-      x_at += kScaleBlock;
-      w_at += kScaleBlock;
+      const int32_t by = b + turn == kb ? kScaleBlock - p.K : kScaleBlock;
+      x_at += by;
+      w_at += by;
     }
     if (b % kScaleSteps == 0) issue_scales();
-    b = b + 1 == kb ? 0 : b + 1;
-  }
-
-  // Load i of kLoads of the block, into a stage of the ring.
-  __device__ __forceinline__ void issue(int stage, int i, const uint8_t* x_from,
-                                        const uint8_t* w_from) const {
-    const uint32_t to = ring_at + stage * S::kStageBytes;
-    if (i < S::kXLoads)
-      load_lds16(to + (wave * S::kXLoads + i) * 1024, x_off[i], x_from);
-    else
-      load_lds16(to + S::kXBytes + (wave * S::kWLoads + i - S::kXLoads) * 1024,
-                 w_off[i - S::kXLoads], w_from);
-  }
-
-  // The first n loads of the next block.
-  __device__ __forceinline__ void issue_block(int stage, int n) {
-    next_block();
+    if (++b == kb) {
+      b = 0;
+      tile += gridDim.x;
+    }
+    const uint32_t to = (uint32_t)(uintptr_t)sh.ring + stage * S::kStageBytes;
     const uint8_t *x_from = uniform_ptr(x_at), *w_from = uniform_ptr(w_at);
 #pragma unroll
-    for (int i = 0; i < S::kLoads; ++i)
-      if (i < n) issue(stage, i, x_from, w_from);
+    for (int i = 0; i < S::kXLoads; ++i)
+      load_lds16(to + (wave * S::kXLoads + i) * 1024, x_off[i], x_from);
+#pragma unroll
+    for (int i = 0; i < S::kWLoads; ++i)
+      load_lds16(to + S::kXBytes + (wave * S::kWLoads + i) * 1024, w_off[i], w_from);
+    stage = stage + 1 == S::kStages ? 0 : stage + 1;
   }
+
+  // Waits until at most LEFT blocks' loads of this wave are in flight (scale
+  // loads between them only make it stricter), then for the workgroup.
+  template <int LEFT>
+  __device__ __forceinline__ void wait_and_meet_blocks() const {
+    if (more())
+      wait_and_meet<LEFT * S::kLoads>();
+    else
+      wait_and_meet<0>();
+  }
+};
+
+// A block's operands in registers, with their scales.
+template <class S>
+struct Block {
+  Codes<S::kGated> x[S::RT], w[S::CT];
+  float sx[S::RT], sw[S::kGated ? 2 : 1];
 };
 
 template <class S>
@@ -512,169 +527,70 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
                                   ? (blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8
                                   : blockIdx.x;
   if (first_tile >= tiles) return;
-  const uint32_t my_tiles = (tiles - 1 - first_tile) / gridDim.x + 1;
-  Loader<S> loads{p, sh, kb, nb, col_tiles, lane, wave, first_tile, (int32_t)my_tiles * kb};
-  loads.ring_at = (uint32_t)(uintptr_t)sh.ring;
+  Loader<S> loads{p, sh, kb, nb, tiles, col_tiles, lane, wave, first_tile};
 
   // Where a wave's squares lie in the tile: token rows of square r, weight
   // rows of square c (gated: gate rows, then up rows).
   constexpr int CH = kGated ? CT / 2 : CT;
-  const auto x_row = [&](int r) MOE_INLINE { return (wr * RT + r) * kSide + lrow; };
-  const auto w_row = [&](int c) MOE_INLINE {
+  const auto x_row = [&](int r) { return (wr * RT + r) * kSide + lrow; };
+  const auto w_row = [&](int c) {
     return (c >= CH ? S::kCols : 0) + wc * CH * kSide + S::channel(c % CH, lrow);
   };
   const int x_k = x_key(lrow), w_k = S::w_key(S::channel(0, lrow));
+  int stage = 0, scale_at = 0;
+  int32_t read_b = 0;
   typename U::Sums acc[CT][RT];
 
-  const auto clear = [&]() MOE_INLINE {
+  const auto clear = [&]() {
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[c][r] = typename U::Sums{};
   };
-  int stored = 0;  // waits to come that a tile's stores may outlast
-  // The block that is read: its place in the ring, its number in its tile,
-  // the place of its scales.
-  int stage = 0, scale_at = 0;
-  int32_t read_b = 0;
-  const auto next_stage = [&]() MOE_INLINE {
+  const auto x_stage = [&]() { return sh.ring + stage * S::kStageBytes; };
+  const auto w_stage = [&]() { return sh.ring + stage * S::kStageBytes + S::kXBytes; };
+  const auto read_scales = [&](Block<S>& blk) {
+    const float* scales = sh.scales[scale_at] + read_b % kScaleSteps;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) blk.sx[r] = scales[x_row(r) * kScaleSteps];
+    blk.sw[0] = scales[(S::kRows + (kGated ? 0 : wc * CT * kSide / kScaleBlock)) * kScaleSteps];
+    if constexpr (kGated) blk.sw[1] = scales[(S::kRows + 1) * kScaleSteps];
+  };
+  const auto block_read = [&]() {
     stage = stage + 1 == kStages ? 0 : stage + 1;
     ++read_b;
     if (read_b % kScaleSteps == 0 || read_b == kb)
-      scale_at = scale_at + 1 == kStages ? 0 : scale_at + 1;
+      scale_at = scale_at + 1 == S::kStages ? 0 : scale_at + 1;
     if (read_b == kb) read_b = 0;
   };
-  const auto read_x = [&](Codes<kGated>& f, int r) MOE_INLINE {
-    read_codes(f, sh.ring + stage * S::kStageBytes, x_row(r), x_k, group);
-  };
-  const auto read_w = [&](Codes<kGated>& f, int c) MOE_INLINE {
-    read_codes(f, sh.ring + stage * S::kStageBytes + S::kXBytes, w_row(c), w_k, group);
-  };
-  struct Scales {
-    float x[RT], w[kGated ? 2 : 1];
-  };
-  const auto read_scales = [&](Scales& f) MOE_INLINE {
-    const float* scales = sh.scales[scale_at] + read_b % kScaleSteps;
+  // Reads a block's operands and multiplies them.
+  const auto multiply = [&]() {
+    const uint8_t *xs = x_stage(), *ws = w_stage();
+    Block<S> blk;
+    read_scales(blk);
+    decltype(as_operand(blk.x[0])) xo[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) f.x[r] = scales[x_row(r) * kScaleSteps];
-    f.w[0] = scales[(S::kRows + (kGated ? 0 : wc * CT * kSide / kScaleBlock)) * kScaleSteps];
-    if constexpr (kGated) f.w[1] = scales[(S::kRows + 1) * kScaleSteps];
-  };
-
-  // One step multiplies one block, square column by square column.  A column's
-  // weights are read (and widened) one or two columns before, the token rows
-  // and the first weights of the block after it in the last two columns, so
-  // the matrix unit never waits for shared memory.  In the middle, when this
-  // block has been read to its end, the workgroup meets once: the next
-  // block's loads have to be there, and this one's place is free for those
-  // of the block kStages further on, which go off one at a time until the
-  // next meeting (sent together, by all waves, they queue for 800 cycles).
-  // What does not need the matrix unit is dealt out between its instructions
-  // in the order written.
-  Codes<kGated> wq[kGated ? 1 : 2], xq[2][RT];
-  Halves wo[kGated ? 2 : 1], xo[kGated ? RT : 1];
-  Scales scale[2];
-  const uint8_t *x_from = nullptr, *w_from = nullptr;   // the loads being sent
-  int to_stage = 0;
-  const auto step = [&](auto parity) MOE_INLINE {
-    constexpr int P = decltype(parity)::value;
-    constexpr int kMeet = (CT - 2) * RT, n = RT * CT;   // squares
-    const auto meet_before = [&](auto at) MOE_INLINE {
-      if constexpr (decltype(at)::value == kMeet) {
-        // In flight stay the loads of the blocks after the next one and, after
-        // a whole tile's stores, those, as long as every load waited for is
-        // older than they are.
-        if (stored > 0) {
-          --stored;
-          wait_and_meet<(kStages - 2) * S::kLoads + S::kStores>();
-        } else {
-          wait_and_meet<(kStages - 2) * S::kLoads>();
+    for (int c = 0; c < CT; ++c) {
+      read_codes(blk.w[c], ws, w_row(c), w_k, group);
+      const auto wo = as_operand(blk.w[c]);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (c == 0) {
+          read_codes(blk.x[r], xs, x_row(r), x_k, group);
+          xo[r] = as_operand(blk.x[r]);
         }
-        to_stage = stage;
-        next_stage();
-        loads.next_block();
-        x_from = uniform_ptr(loads.x_at);
-        w_from = uniform_ptr(loads.w_at);
+        fold(acc[c][r], block_product(wo, xo[r]), blk.sx[r] * blk.sw[c >= CH ? 1 : 0]);
       }
-    };
-    // The share of the loads that goes with part `at` of `parts`.
-    const auto issue_with = [&](auto at, auto parts) MOE_INLINE {
-      constexpr int i = decltype(at)::value, m = decltype(parts)::value;
-      constexpr int l0 = i * S::kLoads / m, l1 = (i + 1) * S::kLoads / m;
-      static_for<l1 - l0>([&](auto l) MOE_INLINE {
-        loads.issue(to_stage, l0 + decltype(l)::value, x_from, w_from);
-      });
-    };
-    if constexpr (!kGated) {
-      // A sum is folded in three instructions after its own, when it is done.
-      f32x4 part[4];
-      static_for<n + 3>([&](auto at) MOE_INLINE {
-        constexpr int i = decltype(at)::value, c = i / RT, r = i % RT;
-        meet_before(at);
-        if constexpr (i < n) {
-          part[i % 4] = block_product(as_operand(wq[c % 2]), as_operand(xq[P][r]));
-          issue_with(std::integral_constant<int, (i + n - kMeet) % n>{},
-                     std::integral_constant<int, n>{});
-          if constexpr (c >= CT - 2) {
-            if constexpr (c == CT - 2) read_x(xq[1 - P][r], r);
-            if constexpr (i == n - 1) read_scales(scale[1 - P]);
-          }
-          if constexpr (r == RT - 1) read_w(wq[c % 2], c + 2 < CT ? c + 2 : c + 2 - CT);
-        }
-        if constexpr (i >= 3) {
-          constexpr int pc = (i - 3) / RT, pr = (i - 3) % RT;
-          fold(acc[pc][pr], part[(i - 3) % 4], scale[P].x[pr] * scale[P].w[0]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      });
-    } else {
-      static_assert(!kGated || RT == 1, "a wave's one row of squares");
-      f32x16 part[2];
-      xo[0] = widen(xq[0][0]);
-      static_for<n>([&](auto at) MOE_INLINE {
-        constexpr int c = decltype(at)::value;
-        meet_before(at);
-        part[c % 2] = f32x16{};
-        static_for<8>([&](auto aj) MOE_INLINE {
-          constexpr int j = decltype(aj)::value;
-          part[c % 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wo[c % 2].h[j], xo[0].h[j],
-                                                               part[c % 2], 0, 0, 0);
-          // The next column's weights, and the codes of the one after it in
-          // their place.
-          wo[(c + 1) % 2].h[j] = widen8(wq[0], j);
-          if constexpr (j % 2 == 1)
-            read_chunk(wq[0], j / 2, sh.ring + stage * S::kStageBytes + S::kXBytes,
-                       w_row(c + 2 < CT ? c + 2 : c + 2 - CT), w_k, group);
-          issue_with(std::integral_constant<int, ((c + 2) % CT) * 8 + j>{},
-                     std::integral_constant<int, CT * 8>{});
-          if constexpr (c == CT - 1 && j == 0) {
-            read_x(xq[0][0], 0);
-            read_scales(scale[1]);
-          }
-          // The sum before is done two instructions on: 3, 3, 3, 3, 2, 2.
-          if constexpr (c > 0 && j >= 2) {
-            constexpr int e0 = j < 6 ? 3 * (j - 2) : 12 + 2 * (j - 6), e1 = e0 + (j < 6 ? 3 : 2);
-            const float f = scale[0].x[0] * scale[0].w[c - 1 >= CH ? 1 : 0];
-            static_for<e1 - e0>([&](auto e) MOE_INLINE {
-              constexpr int k = e0 + decltype(e)::value;
-              acc[c > 0 ? c - 1 : 0][0][k] =
-                  __builtin_fmaf(f, part[(c + 1) % 2][k], acc[c > 0 ? c - 1 : 0][0][k]);
-            });
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        });
-      });
-      fold(acc[CT - 1][0], part[(CT - 1) % 2], scale[0].x[0] * scale[0].w[kGated ? 1 : 0]);
-      scale[0] = scale[1];
     }
+    block_read();
   };
 
   // The sum of a lane's channel i (of kRun) and its token row r.
-  const auto channel_of = [&](int r, int i) MOE_INLINE {
+  const auto channel_of = [&](int r, int i) {
     return acc[i / S::kPer][r][i % S::kPer];
   };
 
-  const auto store_product = [&](const TileAt& at) MOE_INLINE {
+  const auto store_product = [&](const TileAt& at) {
     const int32_t col0 = at.ct * S::kCols;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -697,7 +613,7 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
   };
   // Gated: the activation in the gate's place, each row's largest, then the
   // codes.
-  const auto store_gated = [&](const TileAt& at) MOE_INLINE {
+  const auto store_gated = [&](const TileAt& at) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       uint32_t m = 0;
@@ -737,55 +653,28 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
     }
     meet();  // the maxima's place is free for the next tile
   };
-  const auto end_tile = [&](uint32_t tile) MOE_INLINE {
+  const auto end_tile = [&](uint32_t tile) {
     const TileAt at = locate<S>(p, sh.map, tile, col_tiles);
-    keep_order();  // the stores stay behind the loads sent before
     if constexpr (kGated)
       store_gated(at);
     else
       store_product(at);
-    // Every wave of a whole tile has sent kStores of them (or more).
-    if (at.live == S::kRows && at.ct * S::kCols + S::kCols <= p.cols) stored = S::kStoredWaits;
     clear();
   };
 
   clear();
 #pragma unroll 1
-  for (int i = 0; i < kStages - 1; ++i) loads.issue_block(i, S::kLoads);
-  loads.issue_block(kStages - 1, S::kLoadsAfterMeeting);
-  to_stage = kStages - 1;
-  x_from = uniform_ptr(loads.x_at);
-  w_from = uniform_ptr(loads.w_at);
-  wait_and_meet<(kStages - 2) * S::kLoads + S::kLoadsAfterMeeting>();
-#pragma unroll
-  for (int r = 0; r < RT; ++r) read_x(xq[0][r], r);
-  read_w(wq[0], 0);
-  if constexpr (kGated) {
-    wo[0] = widen(wq[0]);
-    read_w(wq[0], 1);
-  } else {
-    read_w(wq[1], 1);
-  }
-  read_scales(scale[0]);
-  uint32_t tile = first_tile;
-  int32_t b = 0;
-  const auto more = [&]() MOE_INLINE {
-    if (++b < kb) return true;
-    b = 0;
-    end_tile(tile);
-    tile += gridDim.x;
-    return tile < tiles;
-  };
-  for (;;) {
-    step(std::integral_constant<int, 0>{});
-    if (!more()) break;
-    if constexpr (!kGated) {
-      step(std::integral_constant<int, 1>{});
-      if (!more()) break;
+  for (int i = 0; i < kStages - 1; ++i) loads.issue();
+  for (uint32_t tile = first_tile; tile < tiles; tile += gridDim.x) {
+    for (int32_t b = 0; b < kb; ++b) {
+      // This block's loads are done, everyone's, and the block before it is
+      // read: its place takes the next loads.
+      loads.template wait_and_meet_blocks<kStages - 2>();
+      loads.issue();
+      multiply();
     }
+    end_tile(tile);
   }
-  // Nothing is on its way to shared memory when the workgroup ends.
-  __asm__ volatile("s_waitcnt vmcnt(0)" : : : "memory");
 }
 
 constexpr int kComputeUnits = 256;
@@ -805,12 +694,16 @@ hipError_t launch_shape(const ProductArgs& p, int64_t expected_rows, hipStream_t
 
 template <bool GATED>
 hipError_t launch_product(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
-  const int64_t per_expert = expected_rows / p.E;
+  // Rows to expect of an expert choose the tile: few rows leave the weights'
+  // bytes to count, many the squares.
+  const int64_t rows = expected_rows / p.E;
   if constexpr (GATED) {
-    if (per_expert <= 32) return launch_shape<Shape<true, 1, 2, 1, 4, 4>>(p, expected_rows, stream);
-    return launch_shape<Shape<true, 1, 4, 4, 2, 3>>(p, expected_rows, stream);
+    if (rows <= 16) return launch_shape<Shape<true, 1, 2, 1, 4, 4>>(p, expected_rows, stream);
+    if (rows <= 224) return launch_shape<Shape<true, 1, 2, 2, 4, 3>>(p, expected_rows, stream);
+    return launch_shape<Shape<true, 2, 2, 2, 4, 3>>(p, expected_rows, stream);
   } else {
-    if (per_expert <= 32) return launch_shape<Shape<false, 2, 2, 1, 4, 3>>(p, expected_rows, stream);
+    if (rows <= 16) return launch_shape<Shape<false, 2, 2, 1, 4, 3>>(p, expected_rows, stream);
+    if (rows <= 40) return launch_shape<Shape<false, 2, 4, 2, 4, 3>>(p, expected_rows, stream);
     return launch_shape<Shape<false, 4, 4, 2, 4, 3>>(p, expected_rows, stream);
   }
 }

@@ -166,7 +166,8 @@ PRODUCT = dict(x=FAKE, xs=C, cap=CAP, qs=FAKE, w=FAKE, ws=FAKE, counts=FAKE, sen
 @pytest.mark.parametrize("kw", [
     dict(e=0), dict(e=513), dict(k=0), dict(k=100), dict(k=-128), dict(k=65664, xs=65664),
     dict(n=0), dict(n=-128), dict(n=131072, os=131072), dict(n=144 - 8, os=144),
-    dict(cap=-1), dict(cap=(1 << 30) + 1), dict(rows=-1), dict(counts=None), dict(send=None),
+    dict(cap=-1), dict(cap=(1 << 30) + 1), dict(cap=1 << 30, n=1152, os=1152),
+    dict(xs=(1 << 23) + 16), dict(rows=-1), dict(counts=None), dict(send=None),
     dict(counts=None, send=None), dict(x=None), dict(x=FAKE + 8), dict(xs=C - 16), dict(xs=C + 8),
     dict(w=None), dict(w=FAKE + 4), dict(qs=None), dict(qs=FAKE + 2), dict(ws=None),
     dict(out=None), dict(out=FAKE + 2), dict(os=248), dict(os=260),

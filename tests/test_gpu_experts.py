@@ -133,6 +133,25 @@ def test_product_does_not_depend_on_expected_rows(moe):
         assert torch.equal(g.view(torch.int16), got[0].view(torch.int16))
 
 
+@pytest.mark.parametrize("rows", [1, 20, 41])
+def test_product_block_order(moe, rows):
+    """4096 channels begin their sums at a block that follows the output
+    channel; every tile shape adds up alike, also where a start wraps."""
+    inp = Inputs([rows, 0, 3 * rows], 1440, 4096, align=1, exact=True, seed=rows)
+    check_product(moe, inp, True)
+    inp = Inputs([rows, 3], 1440, 4096, align=1, seed=rows)
+    got = [check_product(moe, inp, False, expected_rows=r) for r in (2, 60, 400)]
+    for g in got[1:]:
+        assert torch.equal(g.view(torch.int16), got[0].view(torch.int16))
+
+
+@pytest.mark.parametrize("per_expert", [16, 17, 40, 41])
+def test_product_tile_rules(moe, per_expert):
+    """Rows an expert on both sides of each change of tile, all of them full."""
+    check_product(moe, Inputs([per_expert] * 5, 416, 384, exact=True, seed=per_expert), True,
+                  expected_rows=5 * per_expert)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 17, 64, 300, 1111])
 def test_dense_product(moe, rows):
     """Without counts: one group of every row."""
@@ -281,6 +300,20 @@ def test_gated_strides_and_expected_rows(moe):
     got = [check_gated(moe, inp, r, pad=64) for r in (None, 1, 40, 100, 290, 10 ** 6)]
     for c, s in got[1:]:
         assert torch.equal(c, got[0][0]) and torch.equal(s, got[0][1])
+
+
+@pytest.mark.parametrize("per_expert", [16, 17, 224, 225])
+def test_gated_tile_rules(moe, per_expert):
+    check_gated(moe, Inputs([per_expert] * 2, 512, 384, seed=per_expert),
+                expected_rows=2 * per_expert)
+
+
+def test_gated_block_order(moe):
+    inp = Inputs([3, 0, 60], 2048, 4096, align=1, seed=24)
+    got = [check_gated(moe, inp, r) for r in (3, 63, 3 * 225)]
+    for c, s in got[1:]:
+        assert torch.equal(c[inp.real], got[0][0][inp.real])
+        assert torch.equal(s[inp.real], got[0][1][inp.real])
 
 
 def test_gated_dense(moe):
