@@ -200,7 +200,11 @@ class _OnDevice:
 
 
 def _on_device(fn, dev: int):
-    return _OnDevice(fn, dev) if dev >= 0 else fn
+    """fn for tensors of device `dev`: itself where that is the current one,
+    unless prepare() keeps the call for later."""
+    if dev < 0 or (_get_device() == dev and getattr(_recording, "calls", None) is None):
+        return fn
+    return _OnDevice(fn, dev)
 
 
 class Prepared:
@@ -684,6 +688,19 @@ def moe_combine_fp8(expand_x: torch.Tensor, quant_scales: torch.Tensor, expert_i
     return out
 
 
+def _need_ints(t, n: int, name: str, dev: int) -> None:
+    """A contiguous int32 array of at least n elements on device `dev` (one
+    test for the good case; _need and _need_len say what is wrong)."""
+    try:
+        if (t.dtype is torch.int32 and t.get_device() == dev and t.numel() >= n
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    _need(t, torch.int32, name, device=dev)
+    _need_len(t, n, name)
+
+
 def _product_rows(expand_x, quant_scales, weight, weight_scales, expert_counts, ep_send_counts,
                   dev):
     """The inputs of an experts' product, checked against each other; returns
@@ -693,14 +710,16 @@ def _product_rows(expand_x, quant_scales, weight, weight_scales, expert_counts, 
     if channels == 0 or channels % 128:
         raise ValueError("e4m3 rows need a positive multiple of 128 channels")
     _need(quant_scales, torch.float32, "quant_scales", device=dev)
-    if tuple(quant_scales.shape) != (cap, channels // 128):
+    blocks = channels // 128
+    if quant_scales.shape != (cap, blocks):
         raise ValueError("quant_scales must be [capacity_rows, channels/128]")
     _need(weight, torch.uint8, "weight", device=dev)
-    if weight.dim() != 3 or weight.shape[2] != channels:
-        raise ValueError(f"weight must be [E, N, {channels}], got {list(weight.shape)}")
-    experts, n, _ = weight.shape
+    shape = weight.shape
+    if len(shape) != 3 or shape[2] != channels:
+        raise ValueError(f"weight must be [E, N, {channels}], got {list(shape)}")
+    experts, n, _ = shape
     _need(weight_scales, torch.float32, "weight_scales", device=dev)
-    if tuple(weight_scales.shape) != (experts, (n + 127) // 128, channels // 128):
+    if weight_scales.shape != (experts, (n + 127) // 128, blocks):
         raise ValueError("weight_scales must be [E, ceil(N/128), channels/128]")
     if (expert_counts is None) != (ep_send_counts is None):
         raise ValueError("expert_counts and ep_send_counts go together")
@@ -708,10 +727,8 @@ def _product_rows(expand_x, quant_scales, weight, weight_scales, expert_counts, 
         if experts != 1:
             raise ValueError("a product without expert_counts takes one expert's weight")
     else:
-        _need(expert_counts, torch.int32, "expert_counts", device=dev)
-        _need_len(expert_counts, experts, "expert_counts")
-        _need(ep_send_counts, torch.int32, "ep_send_counts", device=dev)
-        _need_len(ep_send_counts, experts + 1, "ep_send_counts")
+        _need_ints(expert_counts, experts, "expert_counts", dev)
+        _need_ints(ep_send_counts, experts + 1, "ep_send_counts", dev)
     return cap, stride, experts, n, channels
 
 
@@ -735,9 +752,10 @@ def moe_grouped_gemm_fp8(expand_x: torch.Tensor, quant_scales: torch.Tensor,
     cap, xs, experts, n, channels = _product_rows(expand_x, quant_scales, weight, weight_scales,
                                                   expert_counts, ep_send_counts, dev)
     if out is None:
-        out = _new((cap, n), torch.bfloat16, dev)
-    _need(out, torch.bfloat16, "out", contiguous=False, device=dev)
-    out_stride = _need_rows(out, cap, n, "out")
+        out, out_stride = expand_x.new_empty((cap, n), dtype=torch.bfloat16), n
+    else:
+        _need(out, torch.bfloat16, "out", contiguous=False, device=dev)
+        out_stride = _need_rows(out, cap, n, "out")
     status = _status_word(status, check, dev)
     rc = _launch(_on_device(load_library().moe_grouped_gemm_fp8, dev),
         _ptr(expand_x), xs, cap, _ptr(quant_scales), _ptr(weight), _ptr(weight_scales),
@@ -777,13 +795,15 @@ def moe_grouped_gemm_silu_fp8(expand_x: torch.Tensor, quant_scales: torch.Tensor
         raise ValueError("weight must hold 2*I rows an expert, I a positive multiple of 128")
     inter = n // 2
     if out is None:
-        out = _new((cap, inter), torch.uint8, dev)
-    _need(out, torch.uint8, "out", contiguous=False, device=dev)
-    out_stride = _need_rows(out, cap, inter, "out")
+        out, out_stride = expand_x.new_empty((cap, inter)), inter
+    else:
+        _need(out, torch.uint8, "out", contiguous=False, device=dev)
+        out_stride = _need_rows(out, cap, inter, "out")
     if out_scales is None:
-        out_scales = _new((cap, inter // 128), torch.float32, dev)
-    _need(out_scales, torch.float32, "out_scales", device=dev)
-    _need_rows(out_scales, cap, inter // 128, "out_scales")
+        out_scales = quant_scales.new_empty((cap, inter // 128))
+    else:
+        _need(out_scales, torch.float32, "out_scales", device=dev)
+        _need_rows(out_scales, cap, inter // 128, "out_scales")
     status = _status_word(status, check, dev)
     rc = _launch(_on_device(load_library().moe_grouped_gemm_silu_fp8, dev),
         _ptr(expand_x), xs, cap, _ptr(quant_scales), _ptr(weight), _ptr(weight_scales),
@@ -816,7 +836,9 @@ def moe_combine_backward(grad_out: torch.Tensor, expand_x: Optional[torch.Tensor
     if grad_out.dim() != 2:
         raise ValueError("grad_out must be [BS, H]")
     bs, hidden = grad_out.shape
-    k = _routes(expert_ids, expand_idx, ep_send_counts, num_experts, bs, dev)
+    k = _need_ids(expert_ids, bs=bs, device=dev)[1]
+    _need_ints(expand_idx, bs * k, "expand_idx", dev)
+    _need_ints(ep_send_counts, num_experts + 1, "ep_send_counts", dev)
     _need(expert_scales, torch.float32, "expert_scales", device=dev)
     _need_len(expert_scales, bs * k, "expert_scales")
     if not need_expand_x and not need_scales:
@@ -835,17 +857,19 @@ def moe_combine_backward(grad_out: torch.Tensor, expand_x: Optional[torch.Tensor
         _need(expand_x, torch.bfloat16, "expand_x", contiguous=False, device=dev)
         ys = _need_rows(expand_x, capacity_rows, hidden, "expand_x")
         if grad_expert_scales is None:
-            grad_expert_scales = _new((bs, k), torch.float32, dev)
-        _need(grad_expert_scales, torch.float32, "grad_expert_scales", device=dev)
-        if tuple(grad_expert_scales.shape) != (bs, k):
-            raise ValueError(f"grad_expert_scales must be [{bs}, {k}]")
+            grad_expert_scales = expert_scales.new_empty((bs, k))
+        else:
+            _need(grad_expert_scales, torch.float32, "grad_expert_scales", device=dev)
+            if grad_expert_scales.shape != (bs, k):
+                raise ValueError(f"grad_expert_scales must be [{bs}, {k}]")
     else:
         grad_expert_scales = None
     if need_expand_x:
         if grad_expand_x is None:
-            grad_expand_x = _new((capacity_rows, hidden), torch.bfloat16, dev)
-        _need(grad_expand_x, torch.bfloat16, "grad_expand_x", contiguous=False, device=dev)
-        dys = _need_rows(grad_expand_x, capacity_rows, hidden, "grad_expand_x")
+            grad_expand_x, dys = grad_out.new_empty((capacity_rows, hidden)), hidden
+        else:
+            _need(grad_expand_x, torch.bfloat16, "grad_expand_x", contiguous=False, device=dev)
+            dys = _need_rows(grad_expand_x, capacity_rows, hidden, "grad_expand_x")
     else:
         grad_expand_x = None
     status = _status_word(status, check, dev)
@@ -871,7 +895,8 @@ def moe_dispatch_backward(grad_expand_x: torch.Tensor, expert_ids: torch.Tensor,
     and rounded once to bf16 [BS, H]."""
     dev = _need(grad_expand_x, torch.bfloat16, "grad_expand_x", contiguous=False)
     bs, k = _need_ids(expert_ids, device=dev)
-    _routes(expert_ids, expand_idx, ep_send_counts, num_experts, bs, dev)
+    _need_ints(expand_idx, bs * k, "expand_idx", dev)
+    _need_ints(ep_send_counts, num_experts + 1, "ep_send_counts", dev)
     gs = _row_stride(grad_expand_x, "grad_expand_x")
     cap, hidden = grad_expand_x.shape
     add_stride = 0
@@ -879,10 +904,11 @@ def moe_dispatch_backward(grad_expand_x: torch.Tensor, expert_ids: torch.Tensor,
         _need(grad_x_add, torch.bfloat16, "grad_x_add", contiguous=False, device=dev)
         add_stride = _need_rows(grad_x_add, bs, hidden, "grad_x_add")
     if out is None:
-        out = _new((bs, hidden), torch.bfloat16, dev)
-    _need(out, torch.bfloat16, "out", device=dev)
-    if tuple(out.shape) != (bs, hidden):
-        raise ValueError(f"out must be [{bs}, {hidden}], got {list(out.shape)}")
+        out = grad_expand_x.new_empty((bs, hidden))
+    else:
+        _need(out, torch.bfloat16, "out", device=dev)
+        if out.shape != (bs, hidden):
+            raise ValueError(f"out must be [{bs}, {hidden}], got {list(out.shape)}")
     status = _status_word(status, check, dev)
     rc = _launch(_on_device(load_library().moe_dispatch_backward, dev),
         _ptr(grad_expand_x), gs, cap, _ptr(expert_ids), _ptr(expand_idx), _ptr(ep_send_counts),
