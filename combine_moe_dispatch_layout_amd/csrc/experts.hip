@@ -679,6 +679,14 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
 
 constexpr int kComputeUnits = 256;
 
+// Tiles to expect when each expert's last one is half full on average.
+template <class S>
+int64_t tiles_to_expect(const ProductArgs& p, int64_t expected_rows) {
+  const int64_t experts = p.counts ? (expected_rows < p.E ? expected_rows : p.E) : 1;
+  const int64_t row_tiles = (expected_rows + experts * (S::kRows / 2)) / S::kRows;
+  return row_tiles * ((p.cols + S::kCols - 1) / S::kCols);
+}
+
 template <class S>
 hipError_t launch_shape(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
   const int64_t col_tiles = (p.cols + S::kCols - 1) / S::kCols;
@@ -692,20 +700,30 @@ hipError_t launch_shape(const ProductArgs& p, int64_t expected_rows, hipStream_t
   return hipGetLastError();
 }
 
-template <bool GATED>
-hipError_t launch_product(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
-  // Rows to expect of an expert choose the tile: few rows leave the weights'
-  // bytes to count, many the squares.
+// Rows to expect of an expert choose the tile: few rows leave the weights'
+// bytes to count, many the squares.
+hipError_t launch_gated(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
   const int64_t rows = expected_rows / p.E;
-  if constexpr (GATED) {
-    if (rows <= 16) return launch_shape<Shape<true, 1, 2, 1, 4, 4>>(p, expected_rows, stream);
-    if (rows <= 224) return launch_shape<Shape<true, 1, 2, 2, 4, 3>>(p, expected_rows, stream);
-    return launch_shape<Shape<true, 2, 2, 2, 4, 3>>(p, expected_rows, stream);
-  } else {
-    if (rows <= 16) return launch_shape<Shape<false, 2, 2, 1, 4, 3>>(p, expected_rows, stream);
-    if (rows <= 40) return launch_shape<Shape<false, 2, 4, 2, 4, 3>>(p, expected_rows, stream);
-    return launch_shape<Shape<false, 4, 4, 2, 4, 3>>(p, expected_rows, stream);
-  }
+  if (rows <= 16) return launch_shape<Shape<true, 1, 2, 1, 4, 4>>(p, expected_rows, stream);
+  if (rows <= 224) return launch_shape<Shape<true, 1, 2, 2, 4, 3>>(p, expected_rows, stream);
+  return launch_shape<Shape<true, 2, 2, 2, 4, 3>>(p, expected_rows, stream);
+}
+
+hipError_t launch_plain(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
+  using Half = Shape<false, 4, 4, 2, 4, 3>;   // 128 x 256
+  using Full = Shape<false, 4, 8, 4, 2, 2>;   // 256 x 256
+  const int64_t rows = expected_rows / p.E;
+  if (rows <= 16) return launch_shape<Shape<false, 2, 2, 1, 4, 3>>(p, expected_rows, stream);
+  if (rows <= 40) return launch_shape<Shape<false, 2, 4, 2, 4, 3>>(p, expected_rows, stream);
+  // A full tile takes 1.85 times a half one's time (its operands move less)
+  // but leaves more of the last round idle: whichever's rounds are shorter.
+  // 32 experts of 1024 rows, 2048 -> 7168: 668 us half, 617 full; one of
+  // 8192: 150 and 152; one of 4096, 7168 -> 2048 (a half round): 68 and 117.
+  const auto rounds = [](int64_t tiles) { return (tiles + kComputeUnits - 1) / kComputeUnits; };
+  if (rounds(tiles_to_expect<Full>(p, expected_rows)) * 37 <
+      rounds(tiles_to_expect<Half>(p, expected_rows)) * 20)
+    return launch_shape<Full>(p, expected_rows, stream);
+  return launch_shape<Half>(p, expected_rows, stream);
 }
 
 }  // namespace
@@ -728,8 +746,8 @@ hipError_t launch_grouped_gemm(const GroupedGemm& g, hipStream_t stream) {
   p.out_stride = g.out_stride;
   p.out_scales = g.out_scales;
   p.status = g.status;
-  return g.gated ? launch_product<true>(p, g.expected_rows, stream)
-                 : launch_product<false>(p, g.expected_rows, stream);
+  return g.gated ? launch_gated(p, g.expected_rows, stream)
+                 : launch_plain(p, g.expected_rows, stream);
 }
 
 }  // namespace moe

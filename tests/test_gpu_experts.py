@@ -152,6 +152,17 @@ def test_product_tile_rules(moe, per_expert):
                   expected_rows=5 * per_expert)
 
 
+@pytest.mark.parametrize("counts", [[1100], [600, 0, 1, 499], [1, 256, 257, 511, 75]])
+def test_product_large_tiles(moe, counts):
+    """Enough tiles that the largest shape is taken; the others agree with it."""
+    check_product(moe, Inputs(counts, 7456, 256, align=16, exact=True, extra=5, seed=11), True,
+                  expected_rows=1100)
+    inp = Inputs(counts, 7456, 384, align=1, seed=12)
+    got = [check_product(moe, inp, False, expected_rows=r) for r in (1100, 300, 1)]
+    for g in got[1:]:
+        assert torch.equal(g[inp.real].view(torch.int16), got[0][inp.real].view(torch.int16))
+
+
 @pytest.mark.parametrize("rows", [1, 2, 17, 64, 300, 1111])
 def test_dense_product(moe, rows):
     """Without counts: one group of every row."""
