@@ -159,6 +159,7 @@ int product_call(const moe::GroupedGemm& g, void* stream) {
   if (!row_ok(g.x, g.x_stride, g.in_features, 1)) return MOE_ERR_INVALID_ARG;
   if (g.x_stride > moe::kMaxProductStride) return MOE_ERR_INVALID_ARG;
   if (!row_ok(g.out, g.out_stride, g.out_features, g.gated ? 1 : 2)) return MOE_ERR_INVALID_ARG;
+  if (g.out == g.x) return MOE_ERR_INVALID_ARG;
   if (g.w == nullptr || !aligned16(g.w)) return MOE_ERR_INVALID_ARG;
   if (!aligned4(g.x_scales) || !aligned4(g.w_scales)) return MOE_ERR_INVALID_ARG;
   if (g.gated && !aligned4(g.out_scales)) return MOE_ERR_INVALID_ARG;

@@ -5,14 +5,31 @@
 // the gated form
 //   h[r, c] = silu(y[r, c]) * y[r, I + c],  quantised to e4m3 per 128 channels.
 //
-// One matrix instruction multiplies a whole 128-channel block (16 x 16 x
-// 128, e4m3 operands, fp32 sums), so each block's partial sum starts from
-// zero in the instruction and one fused multiply-add per element folds it,
-// with its two scales, into the running fp32 sum.  The weights are the
-// instruction's first operand: a lane then holds four consecutive output
-// channels of ONE row, so the row's scale is one register per lane, the
-// weights' scale is the same for the whole wave, and the output leaves in
-// 8-byte stores.
+// A block's partial sum starts from zero in the matrix unit, and one fused
+// multiply-add per element folds it, with its two scales, into the running
+// fp32 sum.  The weights are the instruction's first operand: a lane then
+// holds output channels of ONE row, so the row's scale is one register per
+// lane, the weights' scale is the same for the whole wave, and a lane's
+// output is 16 neighbouring bytes.
+//
+// The plain product multiplies e4m3 in the matrix unit (16 x 16 x 128, a
+// block an instruction).  Its sums keep 13 bits below the largest of 8
+// products, which a bf16 output does not show; the gated form's fp32 scales
+// would (1.3e-5 off), so there the codes are widened, exactly, to fp16
+// (32 x 32 x 16; 1e-7) at 40 % of the rate.
+//
+// One workgroup a compute unit stays for the whole launch and walks tiles, so
+// that a tile's first loads are under way while the one before is finished.
+// Operands go from memory to a ring of stages in shared memory without
+// passing registers.  Few rows an expert: the weights' bytes bound it
+// (128 tokens on 256 experts, 2048 -> 7168: 619 us, 6.0 TB/s; gated 7168 ->
+// 2 * 2048: 1214 us, 6.1 TB/s; a card-wide read reaches 6.0).  Many: the
+// matrix unit's power does, which lowers the clock to 1.9 - 2.0 GHz, and what
+// moving the operands adds to it (32 experts of 1024 rows, gated: 1.91 ms, 1010
+// TFLOP/s; with operands from the first cache 1.60 ms at 2.3 GHz; plain
+// 4096 x 2048 -> 7168: 76 us, 1590 TFLOP/s).  Between the two, 128 rows an
+// expert on average, 1.00 ms is what 0.86 ms of loads and 0.74 ms of
+// products take together.
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -288,7 +305,9 @@ __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
 
 // ---- the kernel -------------------------------------------------------------------
 constexpr int kScaleSteps = 4;  // blocks whose scales are loaded together
-constexpr int kRowGroup = 8;    // row tiles that walk the columns together
+// Row tiles that walk the columns together, so that an XCD's 32 workgroups
+// share rows and weights in its L2 (4 and 16 measure the same, 2 costs 2 %).
+constexpr int kRowGroup = 8;
 constexpr int kTurnStride = 4096;
 constexpr int kTurnCols = 256;  // channels whose sums begin at the same block
 constexpr int kTurnBlocks = 7;  // and how much further on the next ones do
@@ -701,7 +720,13 @@ hipError_t launch_shape(const ProductArgs& p, int64_t expected_rows, hipStream_t
 }
 
 // Rows to expect of an expert choose the tile: few rows leave the weights'
-// bytes to count, many the squares.
+// bytes to count, many the squares.  Times in us of 64 experts, 4096 -> 1536,
+// with 8 / 32 / 64 / 187 / 256 rows each by tiles of
+//   gated  32 rows: 182 / 202 / 262 / 614 / 799    64: 186 / 189 / 225 / 447 / 583
+//         128 rows: 295 / 248 / 247 / 450 / 569
+//   plain, 1536 -> 4096, with 8 / 32 / 48 / 256 rows
+//          32 rows: 77 / 92 / 102 / 316            64: 77 / 83 / 90 / 205
+//         128 rows: 78 / 85 / 87 / 174
 hipError_t launch_gated(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
   const int64_t rows = expected_rows / p.E;
   if (rows <= 16) return launch_shape<Shape<true, 1, 2, 1, 4, 4>>(p, expected_rows, stream);

@@ -423,8 +423,10 @@ int moe_dispatch_fused_replicated(const void* x, int64_t x_stride, int32_t bs, i
  *   out[r, n] = bf16( sum_b quant_scales[r, b] * weight_scales[e, n/128, b]
  *                       * sum_{c in block b} expand_x[r, c] * weight[e, n, c] )
  *
- * over the 128-channel blocks b of a row, ascending.  Products of codes are
- * exact and the running sum is fp32 (a fused multiply-add per block).  A
+ * over the 128-channel blocks b of a row, ascending (with in_features a
+ * multiple of 4096, from a block that follows n/256 on, and round).
+ * Products of codes are exact and the running sum is fp32 (a fused
+ * multiply-add per block).  A
  * block's own sum is the e4m3 matrix instruction's: it aligns each group of
  * 8 products to the largest and keeps 13 bits below that one's leading bit,
  * then adds in fp32 (measured on N(0,1) rows: 1.3e-5 of the result, against
@@ -439,7 +441,8 @@ int moe_dispatch_fused_replicated(const void* x, int64_t x_stride, int32_t bs, i
  *                     expand_x_stride bytes (>= in_features, a multiple of
  *                     16, at most 2^23), 16-byte aligned: moe_dispatch's
  *                     e4m3 output.
- *  capacity_rows  in  rows of expand_x and out, >= 0, at most 2^30.
+ *  capacity_rows  in  rows of expand_x and out, >= 0, at most 2^30 and at
+ *                     most 2^40 / out_features.
  *  quant_scales   in  fp32 [capacity_rows, in_features/128] row-major.
  *  weight         in  e4m3fn codes [num_experts, out_features, in_features],
  *                     contiguous, 16-byte aligned.
@@ -457,7 +460,8 @@ int moe_dispatch_fused_replicated(const void* x, int64_t x_stride, int32_t bs, i
  *                     chooses launch and tile shapes, never the result.
  *  out            out bf16 [capacity_rows, out_features], row stride
  *                     out_stride elements, 16-byte aligned, stride*2 % 16 ==
- *                     0; must not overlap an input.
+ *                     0; must not overlap an input (expand_x's own address
+ *                     is refused).
  *  status         in/out int32 [1] or NULL: MOE_FLAG_GUARD is OR-ed in when
  *                     a segment leaves [0, capacity_rows) (the rows outside
  *                     are skipped) or segments overlap so far that they hold
@@ -481,7 +485,8 @@ int moe_grouped_gemm_fp8(const void* expand_x, int64_t expand_x_stride, int64_t 
  *   out_scales[r, b] = max_{c in block b} |h[r, c]| / 448
  *   out[r, c] = e4m3( h[r, c] / out_scales[r, b] ), nearest even, saturated
  *
- * over 128-channel blocks b: the format moe_dispatch emits, so out and
+ * (a gate below -87 may give h = 0: its factor is under 2^-125) over
+ * 128-channel blocks b: the format moe_dispatch emits, so out and
  * out_scales are the next product's expand_x and quant_scales.  A block
  * whose scale is 0 has codes 0; a block that holds an infinity or a NaN has
  * that as its scale and NaN codes.

@@ -151,6 +151,7 @@ def test_dispatch_backward_refusals(stub, kw, match):
 # ------------------------------------------------------------------ the C ABI's rules
 
 FAKE = 0x100000  # a non-null, 16-byte aligned address that no refused call touches
+FAKE_OUT = 0x200000
 
 
 @pytest.fixture(scope="module")
@@ -159,7 +160,7 @@ def lib():
 
 
 PRODUCT = dict(x=FAKE, xs=C, cap=CAP, qs=FAKE, w=FAKE, ws=FAKE, counts=FAKE, send=FAKE, e=E, k=C,
-               n=256, rows=0, out=FAKE, os=256, scales=FAKE, status=None, stream=None)
+               n=256, rows=0, out=FAKE_OUT, os=256, scales=FAKE, status=None, stream=None)
 
 
 @pytest.mark.parametrize("gated", [False, True])
@@ -170,7 +171,7 @@ PRODUCT = dict(x=FAKE, xs=C, cap=CAP, qs=FAKE, w=FAKE, ws=FAKE, counts=FAKE, sen
     dict(xs=(1 << 23) + 16), dict(rows=-1), dict(counts=None), dict(send=None),
     dict(counts=None, send=None), dict(x=None), dict(x=FAKE + 8), dict(xs=C - 16), dict(xs=C + 8),
     dict(w=None), dict(w=FAKE + 4), dict(qs=None), dict(qs=FAKE + 2), dict(ws=None),
-    dict(out=None), dict(out=FAKE + 2), dict(os=248), dict(os=260),
+    dict(out=None), dict(out=FAKE_OUT + 2), dict(out=FAKE), dict(os=248), dict(os=260),
 ])
 def test_product_rules(lib, gated, kw):
     a = dict(PRODUCT)
