@@ -90,6 +90,25 @@ def test_combine_backward(moe, bs, hidden, e, k):
     check_combine_backward(moe, Case(moe, bs, hidden, e, k, seed=bs))
 
 
+@pytest.mark.parametrize("bs,hidden,e,k", [(4097, 64, 9, 1), (2049, 1056, 9, 2), (1400, 96, 17, 3),
+                                           (1025, 2016, 30, 4), (900, 160, 30, 5),
+                                           (601, 1024, 64, 8), (500, 64, 40, 9),
+                                           (300, 32, 40, 16)])
+def test_combine_backward_many_short_rows(moe, bs, hidden, e, k):
+    """More than 4096 pairs of fewer than 2048 channels: token by token."""
+    check_combine_backward(moe, Case(moe, bs, hidden, e, k, dropped=0.2, pad=8, seed=k))
+    c = Case(moe, bs, hidden, e, k, repeat=k > 1, align=1, seed=k + 1)
+    dy, dw = check_combine_backward(moe, c)
+    rows = c.rows.to(DEV)
+    dy2, dw2 = moe.moe_combine_backward(c.g.to(DEV), rows, *c.route, c.w.to(DEV), c.e,
+                                        grad_expand_x=rows)
+    at = c.slot[c.real]
+    assert torch.equal(dw2.cpu(), dw) and torch.equal(dy2.cpu()[at], dy[at])
+    none, dw2 = moe.moe_combine_backward(c.g.to(DEV), c.rows.to(DEV), *c.route, c.w.to(DEV), c.e,
+                                         need_expand_x=False)
+    assert torch.equal(dw2.cpu(), dw)
+
+
 @pytest.mark.parametrize("dropped", [0.3, 1.0])
 def test_combine_backward_dropped_pairs(moe, dropped):
     c = Case(moe, 90, 160, 20, 4, dropped=dropped, seed=3)

@@ -175,6 +175,12 @@ def test_dense_product(moe, rows):
     assert tuple(empty.shape) == (0, 352)
 
 
+@pytest.mark.parametrize("n,channels", [(32, 65536), (65536, 128)])
+def test_product_largest_features(moe, n, channels):
+    check_product(moe, Inputs([3, 0, 18], n, channels, align=1, exact=True, seed=51), True,
+                  expected_rows=21)
+
+
 def test_product_non_finite_values_reach_their_own_outputs_only(moe):
     inp = Inputs([40, 40], 128, 256, exact=True, seed=9)
     clean = check_product(moe, inp, True)
@@ -325,6 +331,11 @@ def test_gated_block_order(moe):
     for c, s in got[1:]:
         assert torch.equal(c[inp.real], got[0][0][inp.real])
         assert torch.equal(s[inp.real], got[0][1][inp.real])
+
+
+@pytest.mark.parametrize("inter,channels", [(128, 65536), (32768, 128)])
+def test_gated_largest_features(moe, inter, channels):
+    check_gated(moe, Inputs([2, 17], 2 * inter, channels, align=1, seed=52), expected_rows=19)
 
 
 def test_gated_dense(moe):
