@@ -261,14 +261,23 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // look inside: the five wait states that a scalar address needs after a
 // vector instruction (a readfirstlane) has written it are here.  M0 is the loads' own:
 // nothing else in these kernels uses it.
+// ONCE: bytes that no other workgroup will ask for, marked non-temporal.
+template <bool ONCE>
 __device__ __forceinline__ void load_lds16(uint32_t lds_base, uint32_t offset, const void* base) {
-  __asm__ volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 4\n\t"
-      "global_load_lds_dwordx4 %1, %2"
-      :
-      : "s"(uniform((int)lds_base)), "v"(offset), "s"(base)
-      : "memory");
+  if constexpr (ONCE)
+    __asm__ volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 4\n\t"
+        "global_load_lds_dwordx4 %1, %2 nt"
+        :
+        : "s"(uniform((int)lds_base)), "v"(offset), "s"(base));
+  else
+    __asm__ volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 4\n\t"
+        "global_load_lds_dwordx4 %1, %2"
+        :
+        : "s"(uniform((int)lds_base)), "v"(offset), "s"(base));
 }
 
 __device__ __forceinline__ void load_lds4(uint32_t lds_base, const void* addr) {
@@ -316,9 +325,11 @@ constexpr int kTurnBlocks = 7;  // and how much further on the next ones do
 // weight rows.  Gated, half of a wave's weight rows are gate rows and half
 // the up rows of the same channels.  STAGES blocks have a place in shared
 // memory: the one that is multiplied and those whose loads are under way.
-template <bool GATED_, int RT_, int CT_, int WR_, int WC_, int STAGES_>
+// ONCE: so few rows an expert that one row tile has them all, and its weights
+// are read once.
+template <bool GATED_, int RT_, int CT_, int WR_, int WC_, int STAGES_, bool ONCE_>
 struct Shape {
-  static constexpr bool kGated = GATED_;
+  static constexpr bool kGated = GATED_, kOnce = ONCE_;
   static constexpr int RT = RT_, CT = CT_, WR = WR_, WC = WC_, kStages = STAGES_;
   using U = Unit<kGated>;
   static constexpr int kSide = U::kSide;
@@ -422,6 +433,8 @@ struct Loader {
   uint32_t tile;
   int32_t b = 0;
   int stage = 0, scale_at = 0;
+  uint32_t to = 0;
+  const uint8_t *x_from = nullptr, *w_from = nullptr;
   TileAt at = {};
   uint32_t x_off[S::kXLoads], w_off[S::kWLoads];
   const uint8_t *x_at = nullptr, *w_at = nullptr;
@@ -482,40 +495,37 @@ struct Loader {
     scale_at = scale_at + 1 == S::kStages ? 0 : scale_at + 1;
   }
 
-  // Sends off the next block's loads, if there is one; its scales' first.
-  __device__ __forceinline__ void issue() {
-    if (!more()) return;
-    if (b == 0) {
-      begin_tile();
-    } else {
-      const int32_t by = b + turn == kb ? kScaleBlock - p.K : kScaleBlock;
-      x_at += by;
-      w_at += by;
+  // Turns to the next block and sends off its scales' loads.  Behind the last
+  // block the last one's loads are repeated, into stages nobody reads: every
+  // wave then has the same number in flight at every wait.
+  __device__ __forceinline__ void next() {
+    if (more()) {
+      if (b == 0) {
+        begin_tile();
+      } else {
+        const int32_t by = b + turn == kb ? kScaleBlock - p.K : kScaleBlock;
+        x_at += by;
+        w_at += by;
+      }
+      if (b % kScaleSteps == 0) issue_scales();
+      if (++b == kb) {
+        b = 0;
+        tile += gridDim.x;
+      }
     }
-    if (b % kScaleSteps == 0) issue_scales();
-    if (++b == kb) {
-      b = 0;
-      tile += gridDim.x;
-    }
-    const uint32_t to = (uint32_t)(uintptr_t)sh.ring + stage * S::kStageBytes;
-    const uint8_t *x_from = uniform_ptr(x_at), *w_from = uniform_ptr(w_at);
-#pragma unroll
-    for (int i = 0; i < S::kXLoads; ++i)
-      load_lds16(to + (wave * S::kXLoads + i) * 1024, x_off[i], x_from);
-#pragma unroll
-    for (int i = 0; i < S::kWLoads; ++i)
-      load_lds16(to + S::kXBytes + (wave * S::kWLoads + i) * 1024, w_off[i], w_from);
+    to = (uint32_t)(uintptr_t)sh.ring + stage * S::kStageBytes;
+    x_from = uniform_ptr(x_at);
+    w_from = uniform_ptr(w_at);
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
   }
 
-  // Waits until at most LEFT blocks' loads of this wave are in flight (scale
-  // loads between them only make it stricter), then for the workgroup.
-  template <int LEFT>
-  __device__ __forceinline__ void wait_and_meet_blocks() const {
-    if (more())
-      wait_and_meet<LEFT * S::kLoads>();
+  // Sends off load i of that block's S::kLoads.
+  __device__ __forceinline__ void load(int i) const {
+    if (i < S::kXLoads)
+      load_lds16<false>(to + (wave * S::kXLoads + i) * 1024, x_off[i], x_from);
     else
-      wait_and_meet<0>();
+      load_lds16<S::kOnce>(to + S::kXBytes + (wave * S::kWLoads + i - S::kXLoads) * 1024,
+                           w_off[i - S::kXLoads], w_from);
   }
 };
 
@@ -582,7 +592,9 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
       scale_at = scale_at + 1 == S::kStages ? 0 : scale_at + 1;
     if (read_b == kb) read_b = 0;
   };
-  // Reads a block's operands and multiplies them.
+  // Reads a block's operands and multiplies them, with the next loads in
+  // between: a load takes the address unit 16 cycles, and a wave that sends
+  // all of its own at once waits there for everyone's.
   const auto multiply = [&]() {
     const uint8_t *xs = x_stage(), *ws = w_stage();
     Block<S> blk;
@@ -599,6 +611,11 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
           xo[r] = as_operand(blk.x[r]);
         }
         fold(acc[c][r], block_product(wo, xo[r]), blk.sx[r] * blk.sw[c >= CH ? 1 : 0]);
+        constexpr int kSquares = RT * CT;
+        const int sq = c * RT + r;
+#pragma unroll
+        for (int i = sq * S::kLoads / kSquares; i < (sq + 1) * S::kLoads / kSquares; ++i)
+          loads.load(i);
       }
     }
     block_read();
@@ -683,17 +700,23 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
 
   clear();
 #pragma unroll 1
-  for (int i = 0; i < kStages - 1; ++i) loads.issue();
+  for (int i = 0; i < kStages - 1; ++i) {
+    loads.next();
+#pragma unroll
+    for (int l = 0; l < S::kLoads; ++l) loads.load(l);
+  }
   for (uint32_t tile = first_tile; tile < tiles; tile += gridDim.x) {
     for (int32_t b = 0; b < kb; ++b) {
-      // This block's loads are done, everyone's, and the block before it is
-      // read: its place takes the next loads.
-      loads.template wait_and_meet_blocks<kStages - 2>();
-      loads.issue();
+      // This block's loads are done, everyone's (scale loads between them
+      // only make the wait stricter), and the block before it is read: its
+      // place takes the next loads.
+      wait_and_meet<(kStages - 2) * S::kLoads>();
+      loads.next();
       multiply();
     }
     end_tile(tile);
   }
+  wait_and_meet<0>();  // shared memory is given back with no load under way
 }
 
 constexpr int kComputeUnits = 256;
@@ -720,26 +743,29 @@ hipError_t launch_shape(const ProductArgs& p, int64_t expected_rows, hipStream_t
 }
 
 // Rows to expect of an expert choose the tile: few rows leave the weights'
-// bytes to count, many the squares.  Times in us of 64 experts, 4096 -> 1536,
-// with 8 / 32 / 64 / 187 / 256 rows each by tiles of
-//   gated  32 rows: 182 / 202 / 262 / 614 / 799    64: 186 / 189 / 225 / 447 / 583
-//         128 rows: 295 / 248 / 247 / 450 / 569
-//   plain, 1536 -> 4096, with 8 / 32 / 48 / 256 rows
-//          32 rows: 77 / 92 / 102 / 316            64: 77 / 83 / 90 / 205
-//         128 rows: 78 / 85 / 87 / 174
+// bytes to count, many the squares.  Times in us of 64 experts by rows an
+// expert and tile:
+//   gated, 4096 -> 1536      8    16    24    32    48    64   128   187   256
+//               32 rows    132   133   155   172   223   267   439   586   798
+//               64 rows    150   153   152   153   175   225   339   447   566
+//              128 rows    207   211   219   215   228   228   327   424   510
+//   plain, 1536 -> 4096
+//               32 rows     64    71    80    99   129   145   231   330   435
+//               64 rows     66    72    74    77    85   107   149   182   221
+//              128 rows     89    79    81    83    88    92   117   139   175
 hipError_t launch_gated(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
   const int64_t rows = expected_rows / p.E;
-  if (rows <= 16) return launch_shape<Shape<true, 1, 2, 1, 4, 4>>(p, expected_rows, stream);
-  if (rows <= 224) return launch_shape<Shape<true, 1, 2, 2, 4, 3>>(p, expected_rows, stream);
-  return launch_shape<Shape<true, 2, 2, 2, 4, 3>>(p, expected_rows, stream);
+  if (rows <= 20) return launch_shape<Shape<true, 1, 2, 1, 4, 4, true>>(p, expected_rows, stream);
+  if (rows <= 96) return launch_shape<Shape<true, 1, 2, 2, 4, 3, false>>(p, expected_rows, stream);
+  return launch_shape<Shape<true, 2, 2, 2, 4, 3, false>>(p, expected_rows, stream);
 }
 
 hipError_t launch_plain(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
-  using Half = Shape<false, 4, 4, 2, 4, 3>;   // 128 x 256
-  using Full = Shape<false, 4, 8, 4, 2, 2>;   // 256 x 256
+  using Half = Shape<false, 4, 4, 2, 4, 3, false>;   // 128 x 256
+  using Full = Shape<false, 4, 8, 4, 2, 2, false>;   // 256 x 256
   const int64_t rows = expected_rows / p.E;
-  if (rows <= 16) return launch_shape<Shape<false, 2, 2, 1, 4, 3>>(p, expected_rows, stream);
-  if (rows <= 40) return launch_shape<Shape<false, 2, 4, 2, 4, 3>>(p, expected_rows, stream);
+  if (rows <= 16) return launch_shape<Shape<false, 2, 2, 1, 4, 3, true>>(p, expected_rows, stream);
+  if (rows <= 48) return launch_shape<Shape<false, 2, 4, 2, 4, 3, true>>(p, expected_rows, stream);
   // A full tile takes 1.85 times a half one's time (its operands move less)
   // but leaves more of the last round idle: whichever's rounds are shorter.
   // 32 experts of 1024 rows, 2048 -> 7168: 668 us half, 617 full; one of

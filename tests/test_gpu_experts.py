@@ -133,7 +133,7 @@ def test_product_does_not_depend_on_expected_rows(moe):
         assert torch.equal(g.view(torch.int16), got[0].view(torch.int16))
 
 
-@pytest.mark.parametrize("rows", [1, 20, 41])
+@pytest.mark.parametrize("rows", [1, 20, 49])
 def test_product_block_order(moe, rows):
     """4096 channels begin their sums at a block that follows the output
     channel; every tile shape adds up alike, also where a start wraps."""
@@ -145,7 +145,7 @@ def test_product_block_order(moe, rows):
         assert torch.equal(g.view(torch.int16), got[0].view(torch.int16))
 
 
-@pytest.mark.parametrize("per_expert", [16, 17, 40, 41])
+@pytest.mark.parametrize("per_expert", [16, 17, 48, 49])
 def test_product_tile_rules(moe, per_expert):
     """Rows an expert on both sides of each change of tile, all of them full."""
     check_product(moe, Inputs([per_expert] * 5, 416, 384, exact=True, seed=per_expert), True,
@@ -319,7 +319,7 @@ def test_gated_strides_and_expected_rows(moe):
         assert torch.equal(c, got[0][0]) and torch.equal(s, got[0][1])
 
 
-@pytest.mark.parametrize("per_expert", [16, 17, 224, 225])
+@pytest.mark.parametrize("per_expert", [20, 21, 96, 97])
 def test_gated_tile_rules(moe, per_expert):
     check_gated(moe, Inputs([per_expert] * 2, 512, 384, seed=per_expert),
                 expected_rows=2 * per_expert)
