@@ -5,133 +5,161 @@
 // and the shared row's gradient is g itself.  The scatter's gradient is the
 // combine's gather-sum with unit weights (combine.hip).
 //
-// A workgroup takes one pair (KMAX 1, `share` = K) or one token: each row of
-// y is read once and each row of dy written once.  Per pair each workgroup
-// has one row in and one row out, and a token's pairs run on one XCD, whose
-// L2 gives them g; per token g is read once and the route's set-up is paid
-// once for K rows.  HBM bounds both: 4096 tokens of 7168 channels, K = 8, take
-// 180 us per pair (1.0 GB at 5.6 TB/s; a copy of 2 GiB reaches 5.0) and 205
-// per token, 128 tokens 9.9 and 27 us; at 1024 channels 4096 tokens take 43
-// and 31 us, 512 tokens 7.3 and 8.5.
+// Each row of y is read once and each row of dy written once; a token's pairs
+// run on one XCD, whose L2 gives them g.  Long rows have a workgroup a pair,
+// short ones (up to 1024 channels, or 2048 where the pairs are many) a group
+// of lanes.  HBM bounds both: 4096 tokens of 7168 channels, K = 8, take 182 to
+// 189 us (1.0 GB at 5.3 to 5.6 TB/s; a copy of 2 GiB reaches 5.0), 128 tokens
+// 9.1; 16384 tokens of 512 channels 54 us (0.55 GB).
 #include "moe_internal.h"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 128;
-// Rows of at least this many 16-byte vectors, and batches of at most this
-// many pairs, go pair by pair (2048 channels: 17.4 against 20.6 us at 1024
-// tokens, 215 against 226 at 16384).
-constexpr int32_t kPerPairVecs = 256;
-constexpr int64_t kPerPairMost = 4096;
+constexpr int kShortThreads = 256;
+// Up to this many pairs every pair has a group of lanes (or a workgroup) of its
+// own; beyond, groups take two.
+constexpr int64_t kFewPairs = 4096;
 
-// g's rows are read once per token, or K times per pair (then worth caching).
-template <bool SHARED>
-__device__ __forceinline__ u32x4 load_grad(const u32x4* p) {
-  if constexpr (SHARED)
-    return *p;
-  else
-    return load_stream(p);
-}
-
-template <int KMAX, int UNROLL>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
-    const u32x4* __restrict__ g, int64_t gs, int32_t share, const u32x4* y, int64_t ys,
-    int64_t cap, const int32_t* __restrict__ ids, const int32_t* __restrict__ idx,
+    const u32x4* __restrict__ g, int64_t gs, const u32x4* y, int64_t ys, int64_t cap,
+    const int32_t* __restrict__ ids, const int32_t* __restrict__ idx,
     const int32_t* __restrict__ send, const float* __restrict__ scales, int32_t nvec, int32_t k,
     int32_t E, u32x4* dy, int64_t dys, float* __restrict__ dw, int32_t* status) {
+  constexpr int UNROLL = 4;
   __shared__ int send_lds[StagedSend<kThreads>::kSlots];
-  __shared__ float sum_lds[kThreads / kWave][KMAX];
-  int32_t t = blockIdx.x;
-  if constexpr (KMAX == 1) {
-    // Workgroups i, i + 8, ... share an XCD's L2: the pairs of a token go
-    // to one of them, which then fetches g's row once.
-    const int32_t set = 8 * share, first = t / set * set, in_set = t - first;
-    if (first + set <= (int32_t)gridDim.x) t = first + in_set % 8 * share + in_set / 8;
-  }
+  __shared__ float sum_lds[kThreads / kWave];
+  // Workgroups i, i + 8, ... share an XCD's L2: the pairs of a token go to
+  // one of them, which then fetches g's row once.
+  int32_t pair = blockIdx.x;
+  const int32_t set = 8 * k, first = pair / set * set, in_set = pair - first;
+  if (first + set <= (int32_t)gridDim.x) pair = first + in_set % 8 * k + in_set / 8;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   PairMeta meta;
-  fetch_pair_meta(meta, t, k, ids, idx, scales);
+  fetch_pair_meta(meta, pair, 1, ids, idx, scales);
   StagedSend<kThreads> staged;
   staged.load(send, E + 1);
   // The first of g does not depend on the route.
-  const u32x4* gt = g + (int64_t)(t / share) * gs;
+  const u32x4* gt = g + (int64_t)(pair / k) * gs;
   u32x4 gv[UNROLL];
 #pragma unroll
-  for (int u = 0; u < UNROLL; ++u) {
-    const int32_t v = threadIdx.x + u * kThreads;
-    gv[u] = load_grad<KMAX == 1>(gt + min(v, nvec - 1));
-  }
+  for (int u = 0; u < UNROLL; ++u) gv[u] = gt[min((int)threadIdx.x + u * kThreads, nvec - 1)];
   keep_order();
   staged.store(send_lds);
   __syncthreads();
-  int64_t slot[KMAX];
-  float w[KMAX];
-  resolve_routes<KMAX>(meta, send_lds, nullptr, k, E, cap, slot, w, status, threadIdx.x < kWave);
+  int64_t slot[1];
+  float w[1];
+  resolve_routes<1>(meta, send_lds, nullptr, 1, E, cap, slot, w, status, threadIdx.x < kWave);
 
-  float dot[KMAX];
-#pragma unroll
-  for (int j = 0; j < KMAX; ++j) dot[j] = 0.0f;
-  for (int32_t v0 = threadIdx.x; v0 < nvec; v0 += kThreads * UNROLL) {
-    u32x4 yv[UNROLL][KMAX];
+  float dot = 0.0f;
+  for (int32_t v0 = threadIdx.x; slot[0] >= 0 && v0 < nvec; v0 += kThreads * UNROLL) {
+    u32x4 yv[UNROLL];
     if (dw) {
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u) {
         const int32_t v = v0 + u * kThreads;
-#pragma unroll
-        for (int j = 0; j < KMAX; ++j)
-          if (slot[j] >= 0 && v < nvec) yv[u][j] = load_stream(y + slot[j] * ys + v);
+        if (v < nvec) yv[u] = load_stream(y + slot[0] * ys + v);
       }
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       const int32_t v = v0 + u * kThreads;
       if (v >= nvec) continue;
-      float gf[8];
+      u32x4 o;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        gf[2 * c] = bf16lo_to_f32(gv[u][c]);
-        gf[2 * c + 1] = bf16hi_to_f32(gv[u][c]);
-      }
-#pragma unroll
-      for (int j = 0; j < KMAX; ++j) {
-        if (slot[j] < 0) continue;
+        const float lo = bf16lo_to_f32(gv[u][c]), hi = bf16hi_to_f32(gv[u][c]);
         if (dw) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            dot[j] = __builtin_fmaf(gf[2 * c], bf16lo_to_f32(yv[u][j][c]), dot[j]);
-            dot[j] = __builtin_fmaf(gf[2 * c + 1], bf16hi_to_f32(yv[u][j][c]), dot[j]);
-          }
+          dot = __builtin_fmaf(lo, bf16lo_to_f32(yv[u][c]), dot);
+          dot = __builtin_fmaf(hi, bf16hi_to_f32(yv[u][c]), dot);
         }
-        if (dy) {
-          u32x4 o;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            o[c] = f32_to_bf16_rne(w[j] * gf[2 * c]) |
-                   (f32_to_bf16_rne(w[j] * gf[2 * c + 1]) << 16);
-          store_stream(o, dy + slot[j] * dys + v);
-        }
+        o[c] = f32_to_bf16_rne(w[0] * lo) | (f32_to_bf16_rne(w[0] * hi) << 16);
       }
+      if (dy) store_stream(o, dy + slot[0] * dys + v);
     }
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const int32_t v = v0 + (UNROLL + u) * kThreads;
-      gv[u] = load_grad<KMAX == 1>(gt + min(v, nvec - 1));
-    }
+    for (int u = 0; u < UNROLL; ++u)
+      gv[u] = gt[min(v0 + (UNROLL + u) * kThreads, nvec - 1)];
   }
   if (!dw) return;
 #pragma unroll
-  for (int j = 0; j < KMAX; ++j) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) dot[j] += __shfl_xor(dot[j], d, kWave);
-    if (lane == 0) sum_lds[wave][j] = dot[j];
-  }
+  for (int d = 1; d < kWave; d <<= 1) dot += __shfl_xor(dot, d, kWave);
+  if (lane == 0) sum_lds[wave] = dot;
   __syncthreads();
-  if ((int)threadIdx.x < k) {
-    float s = 0.0f;
+  if (threadIdx.x == 0) dw[pair] = sum_lds[0] + sum_lds[1];
+}
+
+// Short rows: GROUP lanes take a pair, VECS 16-byte vectors a lane, and each
+// of them PAIRS pairs, so that a wave has many rows in flight.
+template <int GROUP, int VECS, int PAIRS>
+__global__ __launch_bounds__(kShortThreads) void combine_backward_short_kernel(
+    const u32x4* __restrict__ g, int64_t gs, const u32x4* y, int64_t ys, int64_t cap,
+    const int32_t* __restrict__ ids, const int32_t* __restrict__ idx,
+    const int32_t* __restrict__ send, const float* __restrict__ scales, int32_t nvec, int32_t k,
+    int32_t pairs, int32_t E, u32x4* dy, int64_t dys, float* __restrict__ dw, int32_t* status) {
+  constexpr int kGroups = kShortThreads / GROUP;
+  const int lane = threadIdx.x % GROUP;
+  const int32_t first = blockIdx.x * (kGroups * PAIRS) + threadIdx.x / GROUP;
+  int32_t e[PAIRS], r[PAIRS];
+  float w[PAIRS];
 #pragma unroll
-    for (int i = 0; i < kThreads / kWave; ++i) s += sum_lds[i][threadIdx.x];
-    dw[(int64_t)t * k + threadIdx.x] = s;
+  for (int u = 0; u < PAIRS; ++u) {
+    const int32_t at = min(first + u * kGroups, pairs - 1);
+    e[u] = ids[at];
+    r[u] = idx[at];
+    w[u] = dy ? scales[at] : 0.0f;
+  }
+  int64_t slot[PAIRS];
+#pragma unroll
+  for (int u = 0; u < PAIRS; ++u) {
+    slot[u] = -1;
+    if (first + u * kGroups < pairs && e[u] >= 0 && e[u] < E && r[u] >= 0) {
+      const int64_t to = (int64_t)send[e[u]] + r[u];
+      if (to >= 0 && to < cap)
+        slot[u] = to;
+      else if (status && lane == 0)
+        atomicOr(status, (int)MOE_FLAG_GUARD);
+    }
+  }
+  u32x4 gv[PAIRS][VECS], yv[PAIRS][VECS];
+#pragma unroll
+  for (int u = 0; u < PAIRS; ++u) {
+    if (slot[u] < 0) continue;
+    const u32x4* gt = g + (int64_t)((first + u * kGroups) / k) * gs;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int v = lane + i * GROUP;
+      if (v >= nvec) continue;
+      gv[u][i] = gt[v];
+      if (dw) yv[u][i] = load_stream(y + slot[u] * ys + v);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < PAIRS; ++u) {
+    float dot = 0.0f;
+    if (slot[u] >= 0) {
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+        const int v = lane + i * GROUP;
+        if (v >= nvec) continue;
+        u32x4 o;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float lo = bf16lo_to_f32(gv[u][i][c]), hi = bf16hi_to_f32(gv[u][i][c]);
+          if (dw) {
+            dot = __builtin_fmaf(lo, bf16lo_to_f32(yv[u][i][c]), dot);
+            dot = __builtin_fmaf(hi, bf16hi_to_f32(yv[u][i][c]), dot);
+          }
+          o[c] = f32_to_bf16_rne(w[u] * lo) | (f32_to_bf16_rne(w[u] * hi) << 16);
+        }
+        if (dy) store_stream(o, dy + slot[u] * dys + v);
+      }
+    }
+    if (!dw) continue;
+#pragma unroll
+    for (int d = 1; d < GROUP; d <<= 1) dot += __shfl_xor(dot, d, kWave);
+    if (lane == 0 && first + u * kGroups < pairs) dw[first + u * kGroups] = dot;
   }
 }
 
@@ -146,22 +174,42 @@ hipError_t launch_combine_backward(const void* grad_out, int64_t grad_stride, co
   const u32x4* gv = static_cast<const u32x4*>(grad_out);
   const u32x4* yv = static_cast<const u32x4*>(y);
   u32x4* dv = static_cast<u32x4*>(grad_y);
-  const int32_t nvec = hidden / 8;
-#define MOE_COMBINE_BACKWARD(KM, UN, ITEMS, SHARE, KK)                                          \
-  launch_kernel(combine_backward_kernel<KM, UN>, dim3((uint32_t)(ITEMS)), kThreads, stream, gv, \
-                grad_stride / 8, SHARE, yv, y_stride / 8, capacity_rows, ids, expand_idx, send,  \
-                scales, nvec, KK, num_experts, dv, grad_y_stride / 8, grad_scales, status)
-  if (nvec >= kPerPairVecs || (int64_t)bs * k <= kPerPairMost)
-    MOE_COMBINE_BACKWARD(1, 4, bs * k, k, 1);
-  else if (k <= 2)
-    MOE_COMBINE_BACKWARD(2, 2, bs, 1, k);
-  else if (k <= 4)
-    MOE_COMBINE_BACKWARD(4, 1, bs, 1, k);
-  else if (k <= 8)
-    MOE_COMBINE_BACKWARD(8, 1, bs, 1, k);
+  const int32_t nvec = hidden / 8, pairs = bs * k;
+  const bool few = pairs <= kFewPairs;
+#define MOE_SHORT(GROUP, VECS, PAIRS)                                                         \
+  launch_kernel(combine_backward_short_kernel<GROUP, VECS, PAIRS>,                            \
+                dim3((uint32_t)(((int64_t)pairs * GROUP + kShortThreads * PAIRS - 1) /         \
+                                (kShortThreads * PAIRS))),                                    \
+                kShortThreads, stream, gv, grad_stride / 8, yv, y_stride / 8, capacity_rows,  \
+                ids, expand_idx, send, scales, nvec, k, pairs, num_experts, dv,               \
+                grad_y_stride / 8, grad_scales, status)
+  // Times in us, a workgroup a pair against groups of lanes: 3200 pairs of 64
+  // channels 5.3 and 3.6, of 512 6.2 and 4.6, of 1024 7.2 and 6.0, of 2048 9.8
+  // and 10.4; 32768 pairs of 64 27 and 5.0, of 512 33 and 16.5, of 1024 43 and
+  // 31.5, of 2048 60 and 58, of 4096 109 and 115.  Two pairs a group against
+  // one: 32768 pairs of 512 16.5 and 21, of 1024 31.5 and 33.5; 3200 pairs 6.2
+  // and 4.6, 6.9 and 6.0.
+  if (nvec <= 8)
+    MOE_SHORT(8, 1, 1);
+  else if (nvec <= 16)
+    MOE_SHORT(16, 1, 1);
+  else if (nvec <= 32)
+    MOE_SHORT(32, 1, 1);
+  else if (nvec <= 64 && few)
+    MOE_SHORT(64, 1, 1);
+  else if (nvec <= 64)
+    MOE_SHORT(32, 2, 2);
+  else if (nvec <= 128 && few)
+    MOE_SHORT(64, 2, 1);
+  else if (nvec <= 128)
+    MOE_SHORT(64, 2, 2);
+  else if (nvec <= 256 && !few)
+    MOE_SHORT(64, 4, 2);
   else
-    MOE_COMBINE_BACKWARD(16, 1, bs, 1, k);
-#undef MOE_COMBINE_BACKWARD
+    launch_kernel(combine_backward_kernel, dim3((uint32_t)pairs), kThreads, stream, gv,
+                  grad_stride / 8, yv, y_stride / 8, capacity_rows, ids, expand_idx, send,
+                  scales, nvec, k, num_experts, dv, grad_y_stride / 8, grad_scales, status);
+#undef MOE_SHORT
   return hipGetLastError();
 }
 

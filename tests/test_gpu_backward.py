@@ -93,9 +93,11 @@ def test_combine_backward(moe, bs, hidden, e, k):
 @pytest.mark.parametrize("bs,hidden,e,k", [(4097, 64, 9, 1), (2049, 1056, 9, 2), (1400, 96, 17, 3),
                                            (1025, 2016, 30, 4), (900, 160, 30, 5),
                                            (601, 1024, 64, 8), (500, 64, 40, 9),
-                                           (300, 32, 40, 16)])
+                                           (300, 32, 40, 16), (700, 480, 20, 7),
+                                           (200, 768, 12, 4), (1, 512, 16, 16),
+                                           (2049, 2048, 4, 2), (3, 2048, 4, 2)])
 def test_combine_backward_many_short_rows(moe, bs, hidden, e, k):
-    """More than 4096 pairs of fewer than 2048 channels: token by token."""
+    """Both sides of every change of the lanes a pair has."""
     check_combine_backward(moe, Case(moe, bs, hidden, e, k, dropped=0.2, pad=8, seed=k))
     c = Case(moe, bs, hidden, e, k, repeat=k > 1, align=1, seed=k + 1)
     dy, dw = check_combine_backward(moe, c)
