@@ -753,19 +753,37 @@ hipError_t launch_shape(const ProductArgs& p, int64_t expected_rows, hipStream_t
 //               32 rows     64    71    80    99   129   145   231   330   435
 //               64 rows     66    72    74    77    85   107   149   182   221
 //              128 rows     89    79    81    83    88    92   117   139   175
+// Where the small tiles all run at once they are the quickest whatever the rows
+// (4 experts of 225 rows, gated 2048 -> 1024: 21 us, 64-row tiles 24, 128-row
+// 35; one of 1024, plain 2048 -> 2048: 14.8, 15.8 and 21), then those of 64.
 hipError_t launch_gated(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
+  using Large = Shape<true, 2, 2, 2, 4, 3, false>;
+  using Middle = Shape<true, 1, 2, 2, 4, 3, false>;
+  using Small = Shape<true, 1, 2, 1, 4, 4, false>;
+  using SmallOnce = Shape<true, 1, 2, 1, 4, 4, true>;
   const int64_t rows = expected_rows / p.E;
-  if (rows <= 20) return launch_shape<Shape<true, 1, 2, 1, 4, 4, true>>(p, expected_rows, stream);
-  if (rows <= 96) return launch_shape<Shape<true, 1, 2, 2, 4, 3, false>>(p, expected_rows, stream);
-  return launch_shape<Shape<true, 2, 2, 2, 4, 3, false>>(p, expected_rows, stream);
+  if (rows <= 20) return launch_shape<SmallOnce>(p, expected_rows, stream);
+  if (tiles_to_expect<Small>(p, expected_rows) <= kComputeUnits)
+    return launch_shape<Small>(p, expected_rows, stream);
+  if (rows <= 96 || tiles_to_expect<Middle>(p, expected_rows) <= kComputeUnits)
+    return launch_shape<Middle>(p, expected_rows, stream);
+  return launch_shape<Large>(p, expected_rows, stream);
 }
 
 hipError_t launch_plain(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
-  using Half = Shape<false, 4, 4, 2, 4, 3, false>;   // 128 x 256
   using Full = Shape<false, 4, 8, 4, 2, 2, false>;   // 256 x 256
+  using Half = Shape<false, 4, 4, 2, 4, 3, false>;   // 128 x 256
+  using Middle = Shape<false, 2, 4, 2, 4, 3, false>;
+  using MiddleOnce = Shape<false, 2, 4, 2, 4, 3, true>;
+  using Small = Shape<false, 2, 2, 1, 4, 3, false>;  // two of them a compute unit
+  using SmallOnce = Shape<false, 2, 2, 1, 4, 3, true>;
   const int64_t rows = expected_rows / p.E;
-  if (rows <= 16) return launch_shape<Shape<false, 2, 2, 1, 4, 3, true>>(p, expected_rows, stream);
-  if (rows <= 48) return launch_shape<Shape<false, 2, 4, 2, 4, 3, true>>(p, expected_rows, stream);
+  if (rows <= 16) return launch_shape<SmallOnce>(p, expected_rows, stream);
+  if (tiles_to_expect<Small>(p, expected_rows) <= 2 * kComputeUnits)
+    return launch_shape<Small>(p, expected_rows, stream);
+  if (rows <= 48) return launch_shape<MiddleOnce>(p, expected_rows, stream);
+  if (tiles_to_expect<Middle>(p, expected_rows) <= kComputeUnits)
+    return launch_shape<Middle>(p, expected_rows, stream);
   // A full tile takes 1.85 times a half one's time (its operands move less)
   // but leaves more of the last round idle: whichever's rounds are shorter.
   // 32 experts of 1024 rows, 2048 -> 7168: 668 us half, 617 full; one of

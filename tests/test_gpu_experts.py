@@ -152,6 +152,24 @@ def test_product_tile_rules(moe, per_expert):
                   expected_rows=5 * per_expert)
 
 
+def test_product_every_tile(moe):
+    """Each tile the rules know, on rows that fill, straddle and miss them."""
+    rng = np.random.default_rng(61)
+    counts = rng.integers(0, 70, 64)
+    counts[[3, 9, 20]] = [0, 128, 1]
+    inp = Inputs(counts.tolist(), 1056, 256, exact=True, seed=61)
+    for r in (640, 1280, 3840, 8192):
+        check_product(moe, inp, True, expected_rows=r)
+    inp = Inputs(counts.tolist(), 1056, 384, seed=62)
+    got = [check_product(moe, inp, False, expected_rows=r) for r in (640, 1280, 3840, 8192)]
+    for g in got[1:]:
+        assert torch.equal(g.view(torch.int16), got[0].view(torch.int16))
+    few = Inputs([300, 0, 129, 640, 256], 1440, 384, align=1, seed=63)
+    got = [check_product(moe, few, False, expected_rows=r) for r in (None, 500, 60)]
+    for g in got[1:]:
+        assert torch.equal(g.view(torch.int16), got[0].view(torch.int16))
+
+
 @pytest.mark.parametrize("counts", [[1100], [600, 0, 1, 499], [1, 256, 257, 511, 75]])
 def test_product_large_tiles(moe, counts):
     """Enough tiles that the largest shape is taken; the others agree with it."""
@@ -323,6 +341,16 @@ def test_gated_strides_and_expected_rows(moe):
 def test_gated_tile_rules(moe, per_expert):
     check_gated(moe, Inputs([per_expert] * 2, 512, 384, seed=per_expert),
                 expected_rows=2 * per_expert)
+
+
+def test_gated_every_tile(moe):
+    rng = np.random.default_rng(64)
+    counts = rng.integers(0, 128, 16)
+    counts[[2, 5]] = [0, 128]
+    inp = Inputs(counts.tolist(), 2048, 384, seed=64)
+    got = [check_gated(moe, inp, r) for r in (160, 336, 960, 1600)]
+    for c, s in got[1:]:
+        assert torch.equal(c, got[0][0]) and torch.equal(s, got[0][1])
 
 
 def test_gated_block_order(moe):
