@@ -22,14 +22,14 @@
 // that a tile's first loads are under way while the one before is finished.
 // Operands go from memory to a ring of stages in shared memory without
 // passing registers.  Few rows an expert: the weights' bytes bound it
-// (128 tokens on 256 experts, 2048 -> 7168: 619 us, 6.0 TB/s; gated 7168 ->
-// 2 * 2048: 1214 us, 6.1 TB/s; a card-wide read reaches 6.0).  Many: the
-// matrix unit's power does, which lowers the clock to 1.9 - 2.0 GHz, and what
-// moving the operands adds to it (32 experts of 1024 rows, gated: 1.91 ms, 1010
-// TFLOP/s; with operands from the first cache 1.60 ms at 2.3 GHz; plain
-// 4096 x 2048 -> 7168: 76 us, 1590 TFLOP/s).  Between the two, 128 rows an
-// expert on average, 1.00 ms is what 0.86 ms of loads and 0.74 ms of
-// products take together.
+// (128 tokens on 256 experts, 2048 -> 7168: 574 us, 6.5 TB/s; gated 7168 ->
+// 2 * 2048: 1070 us, 6.9 TB/s; without the non-temporal mark 619 and 1214).
+// Many: the matrix unit's power does, which lowers the clock to 1.9 - 2.1 GHz,
+// and what moving the operands adds to it (32 experts of 1024 rows, gated:
+// 1.87 - 1.90 ms, 1020 TFLOP/s; with operands from the first cache 1.60 ms at
+// 2.3 GHz; plain 4096 x 2048 -> 7168: 71 us, 1690 TFLOP/s).  Between the two,
+// 128 rows an expert on average, 0.94 - 0.96 ms is what 0.86 ms of loads and
+// 0.74 ms of products take together.
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -259,8 +259,10 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // wait_and_meet counts them.  (As builtins the compiler would wait for the
 // newest of them before every read of shared memory.)  The compiler does not
 // look inside: the five wait states that a scalar address needs after a
-// vector instruction (a readfirstlane) has written it are here.  M0 is the loads' own:
-// nothing else in these kernels uses it.
+// vector instruction (a readfirstlane) has written it are here.  M0 is the
+// loads' own: nothing else in these kernels uses it.  Reads of shared memory
+// may move across a load: it writes to a stage that is read only behind the
+// next wait_and_meet, which nothing passes.
 // ONCE: bytes that no other workgroup will ask for, marked non-temporal.
 template <bool ONCE>
 __device__ __forceinline__ void load_lds16(uint32_t lds_base, uint32_t offset, const void* base) {
