@@ -109,6 +109,9 @@ def test_combine_backward_many_short_rows(moe, bs, hidden, e, k):
     none, dw2 = moe.moe_combine_backward(c.g.to(DEV), c.rows.to(DEV), *c.route, c.w.to(DEV), c.e,
                                          need_expand_x=False)
     assert torch.equal(dw2.cpu(), dw)
+    dy2, none = moe.moe_combine_backward(c.g.to(DEV), None, *c.route, c.w.to(DEV), c.e,
+                                         need_scales=False, capacity_rows=c.cap)
+    assert none is None and torch.equal(dy2.cpu()[at], dy[at])
 
 
 @pytest.mark.parametrize("dropped", [0.3, 1.0])

@@ -116,6 +116,20 @@ def test_product_row_strides(moe):
     check_product(moe, inp, True, pad=24)
 
 
+def test_product_longest_row_stride(moe):
+    """Rows 2^23 bytes apart, in every tile's height (the sums are exact)."""
+    inp = Inputs([260], 33280, 128, align=1, exact=True, seed=9)
+    x, xs, w, ws, counts, send = inp.gpu
+    far = torch.zeros((260, 1 << 23), dtype=torch.uint8, device=DEV)[:, :128]
+    far.copy_(x)
+    want = inp.product()[0].bfloat16()
+    for n, r in ((33280, 260), (33280, 40), (96, 260), (4096, 260)):
+        got = moe.moe_grouped_gemm_fp8(far, xs, w[:, :n].contiguous(),
+                                       ws[:, :-(-n // 128)].contiguous(), counts, send,
+                                       expected_rows=r, check=True)
+        assert torch.equal(got.cpu(), want[:, :n])
+
+
 @pytest.mark.parametrize("experts", [1, 2, 63, 256, 511, 512])
 def test_product_many_experts(moe, experts):
     rng = np.random.default_rng(experts)
