@@ -250,6 +250,15 @@ __device__ __forceinline__ uint32_t codes4(float h0, float h1, float h2, float h
   return (uint32_t)w;
 }
 
+// A value that the compiler takes to be new here.  What is made of it is made
+// where it is needed, once a tile or a few blocks, and not kept in registers
+// through the products, which have none left (kept values were spilled, and
+// each wait for one drained the loads under way).
+__device__ __forceinline__ int renewed(int v) {
+  __asm__ volatile("" : "+v"(v));
+  return v;
+}
+
 // A value that is the same in every lane, in a scalar register.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -431,7 +440,7 @@ struct Loader {
   Shared<S>& sh;
   int32_t kb, nb;
   uint32_t tiles, col_tiles;
-  int lane, wave;
+  int thread_lane, wave;
   uint32_t tile;
   int32_t b = 0;
   int stage = 0, scale_at = 0;
@@ -446,6 +455,7 @@ struct Loader {
 
   __device__ __forceinline__ void begin_tile() {
     at = locate<S>(p, sh.map, tile, col_tiles);
+    const int lane = renewed(thread_lane);
 #pragma unroll
     for (int i = 0; i < S::kXLoads; ++i) {
       const int row = (wave * S::kXLoads + i) * 8 + (lane >> 3);
@@ -478,6 +488,7 @@ struct Loader {
   // The next kScaleSteps blocks' scales (4 lanes a row; past the last block
   // or row, the last one's again).
   __device__ __forceinline__ void issue_scales() {
+    const int lane = renewed(thread_lane);
     const uint32_t to = (uint32_t)(uintptr_t)sh.scales[scale_at];
     int32_t block = min(b + (lane & (kScaleSteps - 1)), kb - 1) + turn;
     if (block >= kb) block -= kb;
@@ -594,24 +605,26 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
       scale_at = scale_at + 1 == S::kStages ? 0 : scale_at + 1;
     if (read_b == kb) read_b = 0;
   };
-  // Reads a block's operands and multiplies them, with the next loads in
-  // between: a load takes the address unit 16 cycles, and a wave that sends
-  // all of its own at once waits there for everyone's.
+  // Reads a block's operands and multiplies them.  Turning to the next loads
+  // (some 400 cycles) hides behind the first reads, and the loads go in
+  // between the products: each takes the address unit 16 cycles, and a wave
+  // that sends all of its own at once waits there for everyone's.
   const auto multiply = [&]() {
     const uint8_t *xs = x_stage(), *ws = w_stage();
     Block<S> blk;
     read_scales(blk);
     decltype(as_operand(blk.x[0])) xo[RT];
+    read_codes(blk.w[0], ws, w_row(0), w_k, group);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) read_codes(blk.x[r], xs, x_row(r), x_k, group);
+    loads.next();
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-      read_codes(blk.w[c], ws, w_row(c), w_k, group);
+      if (c > 0) read_codes(blk.w[c], ws, w_row(c), w_k, group);
       const auto wo = as_operand(blk.w[c]);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        if (c == 0) {
-          read_codes(blk.x[r], xs, x_row(r), x_k, group);
-          xo[r] = as_operand(blk.x[r]);
-        }
+        if (c == 0) xo[r] = as_operand(blk.x[r]);
         fold(acc[c][r], block_product(wo, xo[r]), blk.sx[r] * blk.sw[c >= CH ? 1 : 0]);
         constexpr int kSquares = RT * CT;
         const int sq = c * RT + r;
@@ -629,10 +642,11 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
   };
 
   const auto store_product = [&](const TileAt& at) {
+    const int lane_ = renewed(lane), lrow = lane_ % kSide, group = lane_ / kSide;
     const int32_t col0 = at.ct * S::kCols;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const int row = x_row(r);
+      const int row = (wr * RT + r) * kSide + lrow;
       if (row >= at.live) continue;
       uint16_t* dst = static_cast<uint16_t*>(p.out) + (at.row0 + row) * p.out_stride;
       // The lane's channels, eight at a time.
@@ -652,6 +666,8 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
   // Gated: the activation in the gate's place, each row's largest, then the
   // codes.
   const auto store_gated = [&](const TileAt& at) {
+    const int lane_ = renewed(lane), lrow = lane_ % kSide, group = lane_ / kSide;
+    const auto x_row = [&](int r) { return (wr * RT + r) * kSide + lrow; };
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       uint32_t m = 0;
@@ -713,7 +729,6 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
       // only make the wait stricter), and the block before it is read: its
       // place takes the next loads.
       wait_and_meet<(kStages - 2) * S::kLoads>();
-      loads.next();
       multiply();
     }
     end_tile(tile);
@@ -786,12 +801,12 @@ hipError_t launch_plain(const ProductArgs& p, int64_t expected_rows, hipStream_t
   if (rows <= 48) return launch_shape<MiddleOnce>(p, expected_rows, stream);
   if (tiles_to_expect<Middle>(p, expected_rows) <= kComputeUnits)
     return launch_shape<Middle>(p, expected_rows, stream);
-  // A full tile takes 1.85 times a half one's time (its operands move less)
+  // A full tile takes 1.65 times a half one's time (its operands move less)
   // but leaves more of the last round idle: whichever's rounds are shorter.
-  // 32 experts of 1024 rows, 2048 -> 7168: 668 us half, 617 full; one of
-  // 8192: 150 and 152; one of 4096, 7168 -> 2048 (a half round): 68 and 117.
+  // 2048 -> 7168, half and full: 32 experts of 1024 rows 631 and 587 us, of 256
+  // 207 and 220; one of 8192 144 and 137; 1408 -> 4224, one of 5000 47 and 53.
   const auto rounds = [](int64_t tiles) { return (tiles + kComputeUnits - 1) / kComputeUnits; };
-  if (rounds(tiles_to_expect<Full>(p, expected_rows)) * 37 <
+  if (rounds(tiles_to_expect<Full>(p, expected_rows)) * 33 <
       rounds(tiles_to_expect<Half>(p, expected_rows)) * 20)
     return launch_shape<Full>(p, expected_rows, stream);
   return launch_shape<Half>(p, expected_rows, stream);
