@@ -626,10 +626,14 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
       for (int r = 0; r < RT; ++r) {
         if (c == 0) xo[r] = as_operand(blk.x[r]);
         fold(acc[c][r], block_product(wo, xo[r]), blk.sx[r] * blk.sw[c >= CH ? 1 : 0]);
-        constexpr int kSquares = RT * CT;
+        // With two stages the block is awaited next: its loads go in the
+        // first half (shared expert's product 74 -> 70 us; with three stages
+        // that costs 2 %).
+        constexpr int kAmong = kStages == 2 ? RT * CT / 2 : RT * CT;
         const int sq = c * RT + r;
 #pragma unroll
-        for (int i = sq * S::kLoads / kSquares; i < (sq + 1) * S::kLoads / kSquares; ++i)
+        for (int i = sq * S::kLoads / kAmong;
+             i < (sq + 1) * S::kLoads / kAmong && i < S::kLoads; ++i)
           loads.load(i);
       }
     }
@@ -801,13 +805,13 @@ hipError_t launch_plain(const ProductArgs& p, int64_t expected_rows, hipStream_t
   if (rows <= 48) return launch_shape<MiddleOnce>(p, expected_rows, stream);
   if (tiles_to_expect<Middle>(p, expected_rows) <= kComputeUnits)
     return launch_shape<Middle>(p, expected_rows, stream);
-  // A full tile takes 1.65 times a half one's time (its operands move less)
+  // A full tile takes 1.6 times a half one's time (its operands move less)
   // but leaves more of the last round idle: whichever's rounds are shorter.
-  // 2048 -> 7168, half and full: 32 experts of 1024 rows 631 and 587 us, of 256
-  // 207 and 220; one of 8192 144 and 137; 1408 -> 4224, one of 5000 47 and 53.
+  // 2048 -> 7168, half and full: 32 experts of 1024 rows 628 and 542 us, of 256
+  // 207 and 210; one of 8192 142 and 135; 1408 -> 4224, one of 5000 49 and 52.
   const auto rounds = [](int64_t tiles) { return (tiles + kComputeUnits - 1) / kComputeUnits; };
-  if (rounds(tiles_to_expect<Full>(p, expected_rows)) * 33 <
-      rounds(tiles_to_expect<Half>(p, expected_rows)) * 20)
+  if (rounds(tiles_to_expect<Full>(p, expected_rows)) * 8 <
+      rounds(tiles_to_expect<Half>(p, expected_rows)) * 5)
     return launch_shape<Full>(p, expected_rows, stream);
   return launch_shape<Half>(p, expected_rows, stream);
 }
