@@ -606,18 +606,21 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
     if (read_b == kb) read_b = 0;
   };
   // Reads a block's operands and multiplies them.  Turning to the next loads
-  // (some 400 cycles) hides behind the first reads, and the loads go in
-  // between the products: each takes the address unit 16 cycles, and a wave
-  // that sends all of its own at once waits there for everyone's.
+  // (some 400 cycles) hides behind the first reads, the scales' where all
+  // registers are wanted (gated: odd batch 57 us behind the operands', 54
+  // behind the scales').  The loads go in between the products: each takes
+  // the address unit 16 cycles, and a wave that sends all of its own at once
+  // waits there for everyone's.
   const auto multiply = [&]() {
     const uint8_t *xs = x_stage(), *ws = w_stage();
     Block<S> blk;
     read_scales(blk);
+    if constexpr (kGated) loads.next();
     decltype(as_operand(blk.x[0])) xo[RT];
     read_codes(blk.w[0], ws, w_row(0), w_k, group);
 #pragma unroll
     for (int r = 0; r < RT; ++r) read_codes(blk.x[r], xs, x_row(r), x_k, group);
-    loads.next();
+    if constexpr (!kGated) loads.next();
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
       if (c > 0) read_codes(blk.w[c], ws, w_row(c), w_k, group);
