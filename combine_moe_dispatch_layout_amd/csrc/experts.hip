@@ -26,10 +26,10 @@
 // 2 * 2048: 1070 us, 6.9 TB/s; without the non-temporal mark 619 and 1214).
 // Many: the matrix unit's power does, which lowers the clock to 1.9 - 2.1 GHz,
 // and what moving the operands adds to it (32 experts of 1024 rows, gated:
-// 1.87 - 1.90 ms, 1020 TFLOP/s; with operands from the first cache 1.60 ms at
-// 2.3 GHz; plain 4096 x 2048 -> 7168: 71 us, 1690 TFLOP/s).  Between the two,
-// 128 rows an expert on average, 0.94 - 0.96 ms is what 0.86 ms of loads and
-// 0.74 ms of products take together.
+// 1.87 - 1.91 ms, 1020 TFLOP/s; with operands from the first cache 1.60 ms at
+// 2.3 GHz; plain 2048 -> 7168: 542 us, 1775 TFLOP/s).  Between the two,
+// 128 rows an expert on average, 0.95 ms is what 0.86 ms of loads and 0.74 ms
+// of products take together.
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -606,16 +606,18 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
     if (read_b == kb) read_b = 0;
   };
   // Reads a block's operands and multiplies them.  Turning to the next loads
-  // (some 400 cycles) hides behind the first reads, the scales' where all
-  // registers are wanted (gated: odd batch 57 us behind the operands', 54
-  // behind the scales').  The loads go in between the products: each takes
+  // (some 400 cycles) hides behind the first reads as far as registers allow:
+  // plain behind the operands', gated behind the scales' (odd batch 57 us
+  // behind the operands', 54 so), gated with four squares a wave before them
+  // (32 experts of 1024 rows 1888, 1874 and 1844).  The loads go in between the products: each takes
   // the address unit 16 cycles, and a wave that sends all of its own at once
   // waits there for everyone's.
   const auto multiply = [&]() {
     const uint8_t *xs = x_stage(), *ws = w_stage();
     Block<S> blk;
+    if constexpr (kGated && RT > 1) loads.next();
     read_scales(blk);
-    if constexpr (kGated) loads.next();
+    if constexpr (kGated && RT == 1) loads.next();
     decltype(as_operand(blk.x[0])) xo[RT];
     read_codes(blk.w[0], ws, w_row(0), w_k, group);
 #pragma unroll
