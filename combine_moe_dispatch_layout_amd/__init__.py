@@ -207,6 +207,17 @@ def _on_device(fn, dev: int):
     return _OnDevice(fn, dev)
 
 
+def _launch_on(dev: int, fn, args) -> None:
+    """Launches fn(*args), whose tensors are on device `dev`, and raises on
+    its error."""
+    if dev >= 0 and _get_device() == dev and getattr(_recording, "calls", None) is None:
+        rc = fn(*args)
+    else:
+        rc = _launch(_on_device(fn, dev), *args)
+    if rc:
+        _check(rc)
+
+
 class Prepared:
     """A library call validated once: calling it repeats the same launch
     (same tensors, same stream) with no argument checks, for tight serving
@@ -701,6 +712,21 @@ def _need_ints(t, n: int, name: str, dev: int) -> None:
     _need_len(t, n, name)
 
 
+def _need_rows_of(t, dtype, rows: int, cols: int, name: str, dev: int) -> int:
+    """_need and _need_rows of a row buffer on device `dev`; returns its row
+    stride."""
+    try:
+        st = t.stride()
+        shape = t.shape
+        if (t.dtype is dtype and t.get_device() == dev and len(st) == 2 and st[1] == 1
+                and shape[1] == cols and shape[0] >= rows):
+            return st[0]
+    except AttributeError:
+        pass
+    _need(t, dtype, name, contiguous=False, device=dev)
+    return _need_rows(t, rows, cols, name)
+
+
 def _product_rows(expand_x, quant_scales, weight, weight_scales, expert_counts, ep_send_counts,
                   dev):
     """The inputs of an experts' product, checked against each other; returns
@@ -754,14 +780,14 @@ def moe_grouped_gemm_fp8(expand_x: torch.Tensor, quant_scales: torch.Tensor,
     if out is None:
         out, out_stride = expand_x.new_empty((cap, n), dtype=torch.bfloat16), n
     else:
-        _need(out, torch.bfloat16, "out", contiguous=False, device=dev)
-        out_stride = _need_rows(out, cap, n, "out")
-    status = _status_word(status, check, dev)
-    rc = _launch(_on_device(load_library().moe_grouped_gemm_fp8, dev),
-        _ptr(expand_x), xs, cap, _ptr(quant_scales), _ptr(weight), _ptr(weight_scales),
-        _ptr(expert_counts), _ptr(ep_send_counts), experts, channels, n,
-        _expected(expected_rows), _ptr(out), out_stride, _ptr(status), _stream(expand_x))
-    _check(rc)
+        out_stride = _need_rows_of(out, torch.bfloat16, cap, n, "out", dev)
+    if status is not None or check:
+        status = _status_word(status, check, dev)
+    _launch_on(dev, load_library().moe_grouped_gemm_fp8, (
+        expand_x.data_ptr(), xs, cap, quant_scales.data_ptr(), weight.data_ptr(),
+        weight_scales.data_ptr(), _ptr(expert_counts), _ptr(ep_send_counts), experts, channels,
+        n, _expected(expected_rows), out.data_ptr(), out_stride, _ptr(status),
+        _stream(expand_x)))
     if check:
         _raise_on_status(status, "moe_grouped_gemm_fp8")
     return out
@@ -797,20 +823,19 @@ def moe_grouped_gemm_silu_fp8(expand_x: torch.Tensor, quant_scales: torch.Tensor
     if out is None:
         out, out_stride = expand_x.new_empty((cap, inter)), inter
     else:
-        _need(out, torch.uint8, "out", contiguous=False, device=dev)
-        out_stride = _need_rows(out, cap, inter, "out")
+        out_stride = _need_rows_of(out, torch.uint8, cap, inter, "out", dev)
     if out_scales is None:
         out_scales = quant_scales.new_empty((cap, inter // 128))
     else:
         _need(out_scales, torch.float32, "out_scales", device=dev)
         _need_rows(out_scales, cap, inter // 128, "out_scales")
-    status = _status_word(status, check, dev)
-    rc = _launch(_on_device(load_library().moe_grouped_gemm_silu_fp8, dev),
-        _ptr(expand_x), xs, cap, _ptr(quant_scales), _ptr(weight), _ptr(weight_scales),
-        _ptr(expert_counts), _ptr(ep_send_counts), experts, channels, inter,
-        _expected(expected_rows), _ptr(out), out_stride, _ptr(out_scales), _ptr(status),
-        _stream(expand_x))
-    _check(rc)
+    if status is not None or check:
+        status = _status_word(status, check, dev)
+    _launch_on(dev, load_library().moe_grouped_gemm_silu_fp8, (
+        expand_x.data_ptr(), xs, cap, quant_scales.data_ptr(), weight.data_ptr(),
+        weight_scales.data_ptr(), _ptr(expert_counts), _ptr(ep_send_counts), experts, channels,
+        inter, _expected(expected_rows), out.data_ptr(), out_stride, out_scales.data_ptr(),
+        _ptr(status), _stream(expand_x)))
     if check:
         _raise_on_status(status, "moe_grouped_gemm_silu_fp8")
     return out, out_scales
@@ -854,8 +879,7 @@ def moe_combine_backward(grad_out: torch.Tensor, expand_x: Optional[torch.Tensor
         raise ValueError("capacity_rows must be >= 0")
     ys = dys = 0
     if need_scales:
-        _need(expand_x, torch.bfloat16, "expand_x", contiguous=False, device=dev)
-        ys = _need_rows(expand_x, capacity_rows, hidden, "expand_x")
+        ys = _need_rows_of(expand_x, torch.bfloat16, capacity_rows, hidden, "expand_x", dev)
         if grad_expert_scales is None:
             grad_expert_scales = expert_scales.new_empty((bs, k))
         else:
@@ -868,17 +892,18 @@ def moe_combine_backward(grad_out: torch.Tensor, expand_x: Optional[torch.Tensor
         if grad_expand_x is None:
             grad_expand_x, dys = grad_out.new_empty((capacity_rows, hidden)), hidden
         else:
-            _need(grad_expand_x, torch.bfloat16, "grad_expand_x", contiguous=False, device=dev)
-            dys = _need_rows(grad_expand_x, capacity_rows, hidden, "grad_expand_x")
+            dys = _need_rows_of(grad_expand_x, torch.bfloat16, capacity_rows, hidden,
+                                "grad_expand_x", dev)
     else:
         grad_expand_x = None
-    status = _status_word(status, check, dev)
-    rc = _launch(_on_device(load_library().moe_combine_backward, dev),
-        _ptr(grad_out), _row_stride(grad_out, "grad_out"),
-        _ptr(expand_x) if need_scales else None, ys, capacity_rows, _ptr(expert_ids),
-        _ptr(expand_idx), _ptr(ep_send_counts), _ptr(expert_scales), bs, hidden, k, num_experts,
-        _ptr(grad_expand_x), dys, _ptr(grad_expert_scales), _ptr(status), _stream(grad_out))
-    _check(rc)
+    if status is not None or check:
+        status = _status_word(status, check, dev)
+    _launch_on(dev, load_library().moe_combine_backward, (
+        grad_out.data_ptr(), _row_stride(grad_out, "grad_out"),
+        expand_x.data_ptr() if need_scales else None, ys, capacity_rows, expert_ids.data_ptr(),
+        expand_idx.data_ptr(), ep_send_counts.data_ptr(), expert_scales.data_ptr(), bs, hidden,
+        k, num_experts, _ptr(grad_expand_x), dys, _ptr(grad_expert_scales), _ptr(status),
+        _stream(grad_out)))
     if check:
         _raise_on_status(status, "moe_combine_backward")
     return grad_expand_x, grad_expert_scales
@@ -901,20 +926,19 @@ def moe_dispatch_backward(grad_expand_x: torch.Tensor, expert_ids: torch.Tensor,
     cap, hidden = grad_expand_x.shape
     add_stride = 0
     if grad_x_add is not None:
-        _need(grad_x_add, torch.bfloat16, "grad_x_add", contiguous=False, device=dev)
-        add_stride = _need_rows(grad_x_add, bs, hidden, "grad_x_add")
+        add_stride = _need_rows_of(grad_x_add, torch.bfloat16, bs, hidden, "grad_x_add", dev)
     if out is None:
         out = grad_expand_x.new_empty((bs, hidden))
     else:
         _need(out, torch.bfloat16, "out", device=dev)
         if out.shape != (bs, hidden):
             raise ValueError(f"out must be [{bs}, {hidden}], got {list(out.shape)}")
-    status = _status_word(status, check, dev)
-    rc = _launch(_on_device(load_library().moe_dispatch_backward, dev),
-        _ptr(grad_expand_x), gs, cap, _ptr(expert_ids), _ptr(expand_idx), _ptr(ep_send_counts),
-        _ptr(grad_x_add), add_stride, bs, hidden, k, num_experts, _ptr(out), _ptr(status),
-        _stream(grad_expand_x))
-    _check(rc)
+    if status is not None or check:
+        status = _status_word(status, check, dev)
+    _launch_on(dev, load_library().moe_dispatch_backward, (
+        grad_expand_x.data_ptr(), gs, cap, expert_ids.data_ptr(), expand_idx.data_ptr(),
+        ep_send_counts.data_ptr(), _ptr(grad_x_add), add_stride, bs, hidden, k, num_experts,
+        out.data_ptr(), _ptr(status), _stream(grad_expand_x)))
     if check:
         _raise_on_status(status, "moe_dispatch_backward")
     return out
