@@ -10,7 +10,7 @@
 // short ones (up to 1024 channels, or 2048 where the pairs are many) a group
 // of lanes.  HBM bounds both: 4096 tokens of 7168 channels, K = 8, take 182 to
 // 189 us (1.0 GB at 5.3 to 5.6 TB/s; a copy of 2 GiB reaches 5.0), 128 tokens
-// 9.1; 16384 tokens of 512 channels 54 us (0.55 GB).
+// 8.9; 16384 tokens of 512 channels 54 us (0.55 GB).
 #include "moe_internal.h"
 
 namespace moe {
@@ -22,6 +22,27 @@ constexpr int kShortThreads = 256;
 // own; beyond, groups take two.
 constexpr int64_t kFewPairs = 4096;
 
+// Eight channels of w * g, rounded to bf16.
+__device__ __forceinline__ u32x4 scaled(const u32x4& g, float w) {
+  u32x4 o;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    o[c] = f32_to_bf16_rne(w * bf16lo_to_f32(g[c])) |
+           (f32_to_bf16_rne(w * bf16hi_to_f32(g[c])) << 16);
+  return o;
+}
+
+__device__ __forceinline__ void add_products(const u32x4& g, const u32x4& y, float& dot) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    dot = __builtin_fmaf(bf16lo_to_f32(g[c]), bf16lo_to_f32(y[c]), dot);
+    dot = __builtin_fmaf(bf16hi_to_f32(g[c]), bf16hi_to_f32(y[c]), dot);
+  }
+}
+
+// dy does not need y: its stores go out while y's loads are under way (128
+// tokens 10.2 -> 9.6 us).  Where dy is y itself, a thread stores only what
+// its own earlier load has asked for.
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     const u32x4* __restrict__ g, int64_t gs, const u32x4* y, int64_t ys, int64_t cap,
     const int32_t* __restrict__ ids, const int32_t* __restrict__ idx,
@@ -62,21 +83,17 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
         if (v < nvec) yv[u] = load_stream(y + slot[0] * ys + v);
       }
     }
+    if (dy) {
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const int32_t v = v0 + u * kThreads;
-      if (v >= nvec) continue;
-      u32x4 o;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float lo = bf16lo_to_f32(gv[u][c]), hi = bf16hi_to_f32(gv[u][c]);
-        if (dw) {
-          dot = __builtin_fmaf(lo, bf16lo_to_f32(yv[u][c]), dot);
-          dot = __builtin_fmaf(hi, bf16hi_to_f32(yv[u][c]), dot);
-        }
-        o[c] = f32_to_bf16_rne(w[0] * lo) | (f32_to_bf16_rne(w[0] * hi) << 16);
+      for (int u = 0; u < UNROLL; ++u) {
+        const int32_t v = v0 + u * kThreads;
+        if (v < nvec) store_stream(scaled(gv[u], w[0]), dy + slot[0] * dys + v);
       }
-      if (dy) store_stream(o, dy + slot[0] * dys + v);
+    }
+    if (dw) {
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u)
+        if (v0 + u * kThreads < nvec) add_products(gv[u], yv[u], dot);
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u)
@@ -91,7 +108,8 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
 }
 
 // Short rows: GROUP lanes take a pair, VECS 16-byte vectors a lane, and each
-// of them PAIRS pairs, so that a wave has many rows in flight.
+// of them PAIRS pairs, so that a wave has many rows in flight.  (Here stores
+// before the products measure the same or slower.)
 template <int GROUP, int VECS, int PAIRS>
 __global__ __launch_bounds__(kShortThreads) void combine_backward_short_kernel(
     const u32x4* __restrict__ g, int64_t gs, const u32x4* y, int64_t ys, int64_t cap,
@@ -143,17 +161,8 @@ __global__ __launch_bounds__(kShortThreads) void combine_backward_short_kernel(
       for (int i = 0; i < VECS; ++i) {
         const int v = lane + i * GROUP;
         if (v >= nvec) continue;
-        u32x4 o;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float lo = bf16lo_to_f32(gv[u][i][c]), hi = bf16hi_to_f32(gv[u][i][c]);
-          if (dw) {
-            dot = __builtin_fmaf(lo, bf16lo_to_f32(yv[u][i][c]), dot);
-            dot = __builtin_fmaf(hi, bf16hi_to_f32(yv[u][i][c]), dot);
-          }
-          o[c] = f32_to_bf16_rne(w[u] * lo) | (f32_to_bf16_rne(w[u] * hi) << 16);
-        }
-        if (dy) store_stream(o, dy + slot[u] * dys + v);
+        if (dw) add_products(gv[u][i], yv[u][i], dot);
+        if (dy) store_stream(scaled(gv[u][i], w[u]), dy + slot[u] * dys + v);
       }
     }
     if (!dw) continue;
