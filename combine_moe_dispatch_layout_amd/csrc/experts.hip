@@ -726,12 +726,16 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
   };
 
   clear();
+  // With fewer blocks than stages to come all of them are waited for here,
+  // and none is repeated yet (16 tokens of 128 channels 7.7 -> 7.2 us).
+  int ahead = 0;
 #pragma unroll 1
-  for (int i = 0; i < kStages - 1; ++i) {
+  for (; ahead < kStages - 1 && loads.more(); ++ahead) {
     loads.next();
 #pragma unroll
     for (int l = 0; l < S::kLoads; ++l) loads.load(l);
   }
+  if (ahead < kStages - 1) wait_and_meet<0>();
   for (uint32_t tile = first_tile; tile < tiles; tile += gridDim.x) {
     for (int32_t b = 0; b < kb; ++b) {
       // This block's loads are done, everyone's (scale loads between them
