@@ -26,9 +26,9 @@
 // 2 * 2048: 1070 us, 6.9 TB/s; without the non-temporal mark 619 and 1214).
 // Many: the matrix unit's power does, which lowers the clock to 1.9 - 2.1 GHz,
 // and what moving the operands adds to it (32 experts of 1024 rows, gated:
-// 1.87 - 1.91 ms, 1020 TFLOP/s; with operands from the first cache 1.60 ms at
+// 1.87 - 1.97 ms, 1020 TFLOP/s; with operands from the first cache 1.60 ms at
 // 2.3 GHz; plain 2048 -> 7168: 542 us, 1775 TFLOP/s).  Between the two,
-// 128 rows an expert on average, 0.95 ms is what 0.86 ms of loads and 0.74 ms
+// 128 rows an expert on average, 0.94 - 1.0 ms is what 0.86 ms of loads and 0.74 ms
 // of products take together.
 #include <type_traits>
 
