@@ -518,7 +518,7 @@ int moe_grouped_gemm_silu_fp8(const void* expand_x, int64_t expand_x_stride,
  * The gradient of shared_expert_x is g itself.  A pair that the combine
  * skipped (id out of range, expand_idx < 0, slot beyond capacity_rows) has
  * grad_expert_scales 0 and no row; rows of no pair are not written.  The
- * sums' order is fixed, so results repeat bit for bit.
+ * sums' order follows bs, k and hidden alone, so results repeat bit for bit.
  *
  *  grad_out       in  bf16 [bs, hidden], row stride grad_out_stride; 16-byte
  *                     aligned, stride*2 % 16 == 0 (as every row buffer here).

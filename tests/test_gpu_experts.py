@@ -367,6 +367,18 @@ def test_gated_every_tile(moe):
         assert torch.equal(c, got[0][0]) and torch.equal(s, got[0][1])
 
 
+def test_gated_half_empty_tiles(moe):
+    """Tiles of 64 rows whose second half, or all but one row, is missing."""
+    rng = np.random.default_rng(65)
+    counts = rng.integers(0, 80, 24)
+    counts[[0, 1, 2, 3, 4, 5]] = [1, 32, 33, 64, 65, 97]
+    inp = Inputs(counts.tolist(), 2048, 384, align=1, seed=65)
+    got = [check_gated(moe, inp, r) for r in (960, 24, 24 * 60)]
+    for c, s in got[1:]:
+        assert torch.equal(c[inp.real], got[0][0][inp.real])
+        assert torch.equal(s[inp.real], got[0][1][inp.real])
+
+
 def test_gated_block_order(moe):
     inp = Inputs([3, 0, 60], 2048, 4096, align=1, seed=24)
     got = [check_gated(moe, inp, r) for r in (3, 63, 3 * 225)]
