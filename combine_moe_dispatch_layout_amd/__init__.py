@@ -773,7 +773,8 @@ def moe_grouped_gemm_fp8(expand_x: torch.Tensor, quant_scales: torch.Tensor,
     the layout's; None for both: one dense product of all rows (E = 1).
     expected_rows (BS*K) chooses the launch shape, never the result; give it
     when the buffer is much larger than the batch.  check=True waits for the
-    GPU and raises MoeStatusError if a segment leaves the buffer."""
+    GPU and raises MoeStatusError if a segment leaves the buffer or two
+    segments share a row (then nothing is written)."""
     dev = _need(expand_x, torch.uint8, "expand_x", contiguous=False)
     cap, xs, experts, n, channels = _product_rows(expand_x, quant_scales, weight, weight_scales,
                                                   expert_counts, ep_send_counts, dev)

@@ -60,16 +60,33 @@ __device__ __forceinline__ void segment_of(const int32_t* __restrict__ counts,
 // The row tiles of all experts, from the device's counts: first[e] is the
 // number of tiles before expert e, first[E] their total.  Sums saturate at
 // kMostTiles, above what disjoint segments of 2^30 rows can make, so counts
-// whose segments overlap cannot wrap them; such counts give no tiles at all.
+// whose segments overlap cannot wrap them; such counts give no tiles at all,
+// since two workgroups would write the same rows.
 constexpr int kMostTiles = 1 << 30;
 
 template <int THREADS>
 struct TileMap {
+  static constexpr int kWaves = THREADS / kWave;
   int first[kMaxExperts + 1];
   int start[kMaxExperts];
   int rows[kMaxExperts];
-  int wave_sum[THREADS / kWave];
+  int wave_sum[kWaves];
+  int wave_end[kWaves];
+  int wave_says[kWaves];
 };
+
+// Whether any thread of the workgroup says so.  Two calls need a barrier
+// between them.
+template <int THREADS>
+__device__ __forceinline__ bool anyone(TileMap<THREADS>& map, bool says) {
+  const bool wave_says = __ballot(says) != 0;
+  if ((threadIdx.x & (kWave - 1)) == 0) map.wave_says[threadIdx.x / kWave] = wave_says;
+  __syncthreads();
+  int any = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / kWave; ++w) any |= map.wave_says[w];
+  return any != 0;
+}
 
 template <int THREADS>
 __device__ __forceinline__ void build_tile_map(TileMap<THREADS>& map,
@@ -78,42 +95,73 @@ __device__ __forceinline__ void build_tile_map(TileMap<THREADS>& map,
                                                int64_t cap, int tile_rows, int32_t* status) {
   constexpr int kPer = (kMaxExperts + THREADS - 1) / THREADS;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  int n[kPer], sum = 0;
+  int start[kPer], rows[kPer], n[kPer], sum = 0, end = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = tid * kPer + i;
-    n[i] = 0;
+    start[i] = rows[i] = n[i] = 0;
     if (e < E) {
       bool cut;
-      segment_of(counts, send, cap, e, map.start[e], map.rows[e], cut);
-      n[i] = (map.rows[e] + tile_rows - 1) / tile_rows;
+      segment_of(counts, send, cap, e, start[i], rows[i], cut);
+      map.start[e] = start[i];
+      map.rows[e] = rows[i];
+      n[i] = (rows[i] + tile_rows - 1) / tile_rows;
       if (cut && status && blockIdx.x == 0) atomicOr(status, (int)MOE_FLAG_GUARD);
     }
     sum = min(sum + n[i], kMostTiles);
+    end = max(end, start[i] + rows[i]);
   }
-  int incl = sum;
+  int incl = sum, high = end;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
-    const int up = __shfl_up(incl, d, kWave);
-    if (lane >= d) incl = min(incl + up, kMostTiles);
+    const int up = __shfl_up(incl, d, kWave), up_end = __shfl_up(high, d, kWave);
+    if (lane >= d) {
+      incl = min(incl + up, kMostTiles);
+      high = max(high, up_end);
+    }
   }
-  if (lane == kWave - 1) map.wave_sum[wave] = incl;
+  int before = __shfl_up(high, 1, kWave);
+  if (lane == 0) before = 0;
+  if (lane == kWave - 1) {
+    map.wave_sum[wave] = incl;
+    map.wave_end[wave] = high;
+  }
   __syncthreads();
   int base = incl - sum, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / kWave; ++w) {
-    if (w < wave) base = min(base + map.wave_sum[w], kMostTiles);
+    if (w < wave) {
+      base = min(base + map.wave_sum[w], kMostTiles);
+      before = max(before, map.wave_end[w]);
+    }
     total = min(total + map.wave_sum[w], kMostTiles);
   }
-  const bool overlap = total > cap / tile_rows + E;
-  if (overlap && status && blockIdx.x == 0 && tid == 0) atomicOr(status, (int)MOE_FLAG_GUARD);
+  // Segments that each start behind all earlier ones, as a layout's do, are
+  // disjoint.
+  bool early = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = tid * kPer + i;
     if (e < E) map.first[e] = base;
     base = min(base + n[i], kMostTiles);
+    early |= rows[i] > 0 && start[i] < before;
+    before = max(before, start[i] + rows[i]);
   }
-  if (tid == 0) map.first[E] = overlap ? 0 : total;
+  if (tid == 0) map.first[E] = total;
+  if (!anyone(map, early)) return;
+  // Others are compared, each with each.
+  bool overlap = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    for (int f = 0; f < E; ++f)
+      overlap |= rows[i] > 0 && map.rows[f] > 0 && f != tid * kPer + i &&
+                 start[i] < map.start[f] + map.rows[f] && map.start[f] < start[i] + rows[i];
+  __syncthreads();
+  if (!anyone(map, overlap)) return;
+  if (tid == 0) {
+    map.first[E] = 0;
+    if (status && blockIdx.x == 0) atomicOr(status, (int)MOE_FLAG_GUARD);
+  }
   __syncthreads();
 }
 
@@ -250,13 +298,14 @@ __device__ __forceinline__ uint32_t codes4(float h0, float h1, float h2, float h
   return (uint32_t)w;
 }
 
-// A value that the compiler takes to be new here.  What is made of it is made
-// where it is needed, once a tile or a few blocks, and not kept in registers
-// through the products, which have none left (kept values were spilled, and
-// each wait for one drained the loads under way).
-__device__ __forceinline__ int renewed(int v) {
-  __asm__ volatile("" : "+v"(v));
-  return v;
+// The lane, counted again where it is asked for.  What is made of it is made
+// where it is needed, once a tile or a few blocks, and neither is kept in
+// registers through the products, which have none left (kept values were
+// spilled, and each wait for one drained the loads under way).
+__device__ __forceinline__ int lane_again() {
+  int none = 0;
+  __asm__ volatile("" : "+v"(none));  // new to the compiler
+  return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, none));
 }
 
 // A value that is the same in every lane, in a scalar register.
@@ -407,7 +456,7 @@ __device__ __forceinline__ TileAt locate(const ProductArgs& p, const TileMap<S::
                                          uint32_t tile, uint32_t col_tiles) {
   const int t = (int)(tile / col_tiles);
   // The number of experts whose tiles end at or before t.
-  const int lane = threadIdx.x & (kWave - 1);
+  const int lane = lane_again();
   int e = 0;
   for (int i = 0; i < p.E; i += kWave) {
     const bool before = i + lane < p.E && map.first[i + lane + 1] <= t;
@@ -440,7 +489,7 @@ struct Loader {
   Shared<S>& sh;
   int32_t kb, nb;
   uint32_t tiles, col_tiles;
-  int thread_lane, wave;
+  int wave;
   uint32_t tile;
   int32_t b = 0;
   int stage = 0, scale_at = 0;
@@ -455,7 +504,7 @@ struct Loader {
 
   __device__ __forceinline__ void begin_tile() {
     at = locate<S>(p, sh.map, tile, col_tiles);
-    const int lane = renewed(thread_lane);
+    const int lane = lane_again();
 #pragma unroll
     for (int i = 0; i < S::kXLoads; ++i) {
       const int row = (wave * S::kXLoads + i) * 8 + (lane >> 3);
@@ -488,7 +537,7 @@ struct Loader {
   // The next kScaleSteps blocks' scales (4 lanes a row; past the last block
   // or row, the last one's again).
   __device__ __forceinline__ void issue_scales() {
-    const int lane = renewed(thread_lane);
+    const int lane = lane_again();
     const uint32_t to = (uint32_t)(uintptr_t)sh.scales[scale_at];
     int32_t block = min(b + (lane & (kScaleSteps - 1)), kb - 1) + turn;
     if (block >= kb) block -= kb;
@@ -569,7 +618,7 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
                                   ? (blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8
                                   : blockIdx.x;
   if (first_tile >= tiles) return;
-  Loader<S> loads{p, sh, kb, nb, tiles, col_tiles, lane, wave, first_tile};
+  Loader<S> loads{p, sh, kb, nb, tiles, col_tiles, wave, first_tile};
 
   // Where a wave's squares lie in the tile: token rows of square r, weight
   // rows of square c (gated: gate rows, then up rows).
@@ -651,7 +700,7 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
   };
 
   const auto store_product = [&](const TileAt& at) {
-    const int lane_ = renewed(lane), lrow = lane_ % kSide, group = lane_ / kSide;
+    const int lane_ = lane_again(), lrow = lane_ % kSide, group = lane_ / kSide;
     const int32_t col0 = at.ct * S::kCols;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -675,7 +724,7 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
   // Gated: the activation in the gate's place, each row's largest, then the
   // codes.
   const auto store_gated = [&](const TileAt& at) {
-    const int lane_ = renewed(lane), lrow = lane_ % kSide, group = lane_ / kSide;
+    const int lane_ = lane_again(), lrow = lane_ % kSide, group = lane_ / kSide;
     const auto x_row = [&](int r) { return (wr * RT + r) * kSide + lrow; };
 #pragma unroll
     for (int r = 0; r < RT; ++r) {

@@ -464,8 +464,8 @@ int moe_dispatch_fused_replicated(const void* x, int64_t x_stride, int32_t bs, i
  *                     is refused).
  *  status         in/out int32 [1] or NULL: MOE_FLAG_GUARD is OR-ed in when
  *                     a segment leaves [0, capacity_rows) (the rows outside
- *                     are skipped) or segments overlap so far that they hold
- *                     more rows than the buffer (then nothing is written).
+ *                     are skipped) or two segments share a row of the buffer
+ *                     (then nothing is written).
  */
 int moe_grouped_gemm_fp8(const void* expand_x, int64_t expand_x_stride, int64_t capacity_rows,
                          const float* quant_scales, const void* weight,
