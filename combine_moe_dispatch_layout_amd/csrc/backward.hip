@@ -21,6 +21,9 @@ constexpr int kShortThreads = 256;
 // Up to this many pairs every pair has a group of lanes (or a workgroup) of its
 // own; beyond, groups take two.
 constexpr int64_t kFewPairs = 4096;
+// A launch has fewer than 2^32 threads, at most 128 a pair: larger batches
+// take several.
+constexpr int64_t kMostPairs = int64_t(1) << 24;
 
 // Eight channels of w * g, rounded to bf16.
 __device__ __forceinline__ u32x4 scaled(const u32x4& g, float w) {
@@ -180,6 +183,19 @@ hipError_t launch_combine_backward(const void* grad_out, int64_t grad_stride, co
                                    const float* scales, int32_t bs, int32_t hidden, int32_t k,
                                    int32_t num_experts, void* grad_y, int64_t grad_y_stride,
                                    float* grad_scales, int32_t* status, hipStream_t stream) {
+  const int32_t most = (int32_t)(kMostPairs / k);  // tokens a launch
+  if (bs > most) {
+    for (int32_t t = 0; t < bs; t += most) {
+      const int64_t p = (int64_t)t * k;
+      const hipError_t err = launch_combine_backward(
+          static_cast<const uint16_t*>(grad_out) + t * grad_stride, grad_stride, y, y_stride,
+          capacity_rows, ids + p, expand_idx + p, send, scales ? scales + p : nullptr,
+          bs - t < most ? bs - t : most, hidden, k, num_experts, grad_y, grad_y_stride,
+          grad_scales ? grad_scales + p : nullptr, status, stream);
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+  }
   const u32x4* gv = static_cast<const u32x4*>(grad_out);
   const u32x4* yv = static_cast<const u32x4*>(y);
   u32x4* dv = static_cast<u32x4*>(grad_y);

@@ -1,0 +1,65 @@
+"""The gradient of combine and dispatch on more tokens than one launch has
+threads for.  Nearly all pairs are dropped (their rows would not fit), and
+live ones sit on both sides of where a launch ends, at the first and at the
+last token.  The values are whole numbers, so every sum is exact."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+K, E = 16, 16
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import combine_moe_dispatch_layout_amd as m
+    m.load_library()
+    assert torch.cuda.is_available()
+    return m
+
+
+def spots(bs, k, edges):
+    """Live pairs: a few tokens around each edge, any of the k places."""
+    tokens = sorted({t for at in edges for t in (at - 1, at, at + 1) if 0 <= t < bs})
+    return [(t, (5 * i + 3) % k) for i, t in enumerate(tokens)]
+
+
+def routes(bs, k, live, cap):
+    """ids and ranks with only `live` pairs kept, pair i at row cap - 1 - i."""
+    ids = torch.zeros((bs, k), dtype=torch.int32, device=DEV)
+    idx = torch.full((bs * k,), -1, dtype=torch.int32, device=DEV)
+    send = torch.arange(E + 1, dtype=torch.int32, device=DEV)
+    for i, (t, j) in enumerate(live):
+        ids[t, j] = i % E
+        idx[t * k + j] = cap - 1 - i - i % E
+    return ids, idx, send
+
+
+@pytest.mark.parametrize("bs,hidden", [((1 << 21) + 3, 2080), ((1 << 23) + 3, 256),
+                                       ((1 << 25) + 3, 64)])
+def test_combine_backward_beyond_one_launch(moe, bs, hidden):
+    """128, 32 and 8 threads a pair: 2^32 of them and more."""
+    live = spots(bs, K, (0, 1 << 20, 1 << 21, 7 << 20, 1 << 23, 1 << 25, bs - 1))
+    cap = len(live) + E
+    gen = torch.Generator().manual_seed(hidden)
+    ids, idx, send = routes(bs, K, live, cap)
+    y = torch.randint(-3, 4, (cap, hidden), generator=gen).to(DEV, torch.bfloat16)
+    g = torch.zeros((bs, hidden), dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros((bs, K), device=DEV)
+    for t, j in live:
+        g[t] = torch.randint(-3, 4, (hidden,), generator=gen).to(DEV, torch.bfloat16)
+        w[t, j] = float(torch.randint(1, 9, (1,), generator=gen))
+    dw = torch.full((bs, K), -1.0, device=DEV)
+    dy = torch.full((cap, hidden), -5.0, dtype=torch.bfloat16, device=DEV)
+    moe.moe_combine_backward(g, y, ids, idx, send, w, E, grad_expand_x=dy,
+                             grad_expert_scales=dw, check=True)
+    want = torch.full((cap, hidden), -5.0, dtype=torch.bfloat16, device=DEV)
+    for i, (t, j) in enumerate(live):
+        row = cap - 1 - i
+        want[row] = (w[t, j] * g[t].float()).bfloat16()
+        assert float(dw[t, j]) == float((g[t].double() * y[row].double()).sum()), (t, j)
+        dw[t, j] = 0.0
+    assert torch.equal(dy, want)
+    assert not dw.any()
