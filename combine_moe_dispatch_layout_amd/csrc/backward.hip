@@ -21,9 +21,9 @@ constexpr int kShortThreads = 256;
 // Up to this many pairs every pair has a group of lanes (or a workgroup) of its
 // own; beyond, groups take two.
 constexpr int64_t kFewPairs = 4096;
-// A launch has fewer than 2^32 threads, at most 128 a pair: larger batches
-// take several.
-constexpr int64_t kMostPairs = int64_t(1) << 24;
+// Pairs of one launch (2^24), of at most a workgroup each: larger batches take
+// several.
+constexpr int32_t kMostPairs = most_items(kThreads);
 
 // Eight channels of w * g, rounded to bf16.
 __device__ __forceinline__ u32x4 scaled(const u32x4& g, float w) {
@@ -183,7 +183,7 @@ hipError_t launch_combine_backward(const void* grad_out, int64_t grad_stride, co
                                    const float* scales, int32_t bs, int32_t hidden, int32_t k,
                                    int32_t num_experts, void* grad_y, int64_t grad_y_stride,
                                    float* grad_scales, int32_t* status, hipStream_t stream) {
-  const int32_t most = (int32_t)(kMostPairs / k);  // tokens a launch
+  const int32_t most = kMostPairs / k;  // tokens a launch
   if (bs > most) {
     for (int32_t t = 0; t < bs; t += most) {
       const int64_t p = (int64_t)t * k;

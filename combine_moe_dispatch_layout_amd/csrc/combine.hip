@@ -212,6 +212,19 @@ hipError_t launch_combine(const void* y, int64_t y_stride, int64_t capacity_rows
   constexpr int kVpt = MOE_COMBINE_VPT;
   const int32_t nvec = hidden / 8;
   const int32_t nchunks = (nvec + kThreads * kVpt - 1) / (kThreads * kVpt);
+  const int32_t most = most_items(kThreads) / nchunks;  // tokens a launch
+  if (bs > most) {
+    for (int32_t t = 0; t < bs; t += most) {
+      const int64_t p = (int64_t)t * k;
+      const hipError_t err = launch_combine(
+          y, y_stride, capacity_rows, ids + p, expand_idx + p, send, scales ? scales + p : nullptr,
+          shared ? static_cast<const uint16_t*>(shared) + t * shared_stride : nullptr,
+          shared_stride, bs - t < most ? bs - t : most, hidden, k, num_experts,
+          static_cast<uint16_t*>(out) + (int64_t)t * hidden, status, stream);
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+  }
   const int32_t n_items = bs * nchunks;
   const dim3 grid((uint32_t)n_items);
   const int kmax = k <= 2 ? 2 : k <= 4 ? 4 : k <= 8 ? 8 : 16;

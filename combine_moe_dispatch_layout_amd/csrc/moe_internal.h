@@ -361,6 +361,10 @@ inline void launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, hipS
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, static_cast<Params>(args)...);
 }
 
+// Workgroups of `threads` that one launch may have: a grid of 2^32 threads or
+// more is not refused but wraps, and only the remainder runs.
+constexpr int32_t most_items(int threads) { return (int32_t)((int64_t(1) << 31) / threads); }
+
 LayoutPlan plan_layout(int32_t bs, int32_t k);
 
 // Read-ahead workgroups only ride along a multi-workgroup layout, and only

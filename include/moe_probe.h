@@ -63,10 +63,11 @@ int moe_probe_stream_mix(const void* src, int64_t src_rows_total, void* dst,
  * (one when a single workgroup ranks the batch); moe_dispatch one, or two (a
  * read-ahead of the token rows, then the scatter) for bf16 output from
  * contiguous rows of 32 to 240 MB; moe_dispatch_fused one (fused kernel, bs*k <= 2048) or two (the
- * layout's ranking launch, then the scatter); moe_combine and
- * moe_combine_fp8 one; moe_combine_backward one, or beyond 2^24 pairs one for
- * each floor(2^24 / k) tokens.  Calls that return an error or have nothing to
- * do launch nothing and leave the pairs bound.
+ * layout's ranking launch, then the scatter); moe_combine, moe_combine_fp8,
+ * the experts' products and the gradients one.  moe_combine and the gradients
+ * take several beyond 2^24 items, of a pair or 1024 channels of a token each.
+ * Calls that return an error or have nothing to do launch nothing and leave
+ * the pairs bound.
  *
  *  n   in  0..16; a new call replaces the pairs still bound, and n = 0 only
  *          drops them.

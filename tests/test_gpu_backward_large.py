@@ -63,3 +63,31 @@ def test_combine_backward_beyond_one_launch(moe, bs, hidden):
         dw[t, j] = 0.0
     assert torch.equal(dy, want)
     assert not dw.any()
+
+
+@pytest.mark.parametrize("bs,hidden,k", [((1 << 25) + 3, 32, 1), ((1 << 24) + 3, 992, 1),
+                                         ((1 << 23) + 3, 1056, 2)])
+def test_dispatch_backward_and_combine_beyond_one_launch(moe, bs, hidden, k):
+    """128 threads a token and 1024 channels: 2^31 and 2^32 of them and more.
+    The combine with weights of two and a shared row runs on the same routes."""
+    live = spots(bs, k, (0, 1 << 22, 1 << 23, 1 << 24, 1 << 25, bs - 1))
+    cap = len(live) + E
+    gen = torch.Generator().manual_seed(hidden)
+    ids, idx, send = routes(bs, k, live, cap)
+    rows = torch.randint(-3, 4, (cap, hidden), generator=gen).to(DEV, torch.bfloat16)
+    add = torch.zeros((bs, hidden), dtype=torch.bfloat16, device=DEV)
+    for t, j in live:
+        add[t] = torch.randint(-3, 4, (hidden,), generator=gen).to(DEV, torch.bfloat16)
+    out = torch.full((bs, hidden), -5.0, dtype=torch.bfloat16, device=DEV)
+    w = torch.full((bs, k), 2.0, device=DEV)
+    for times in (1.0, 2.0):
+        out.fill_(-5.0)
+        if times == 1.0:
+            moe.moe_dispatch_backward(rows, ids, idx, send, E, grad_x_add=add, out=out, check=True)
+        else:
+            moe.moe_combine(rows, ids, idx, send, w, add, E, out=out, check=True)
+        for i, (t, j) in enumerate(live):
+            want = times * rows[cap - 1 - i].float() + add[t].float()
+            assert torch.equal(out[t], want.bfloat16()), t
+            out[t] = 0
+        assert not out.any()
