@@ -247,6 +247,19 @@ hipError_t launch_combine_fp8(const void* y, int64_t y_stride, int64_t capacity_
   const int32_t ngroups = hidden / 16;
   const int32_t threads = ngroups <= 1024 ? (ngroups + kWave - 1) / kWave * kWave : 1024;
   const int32_t nchunks = (ngroups + threads - 1) / threads;
+  const int32_t most = most_items(threads) / nchunks;  // tokens a launch
+  if (bs > most) {
+    for (int32_t t = 0; t < bs; t += most) {
+      const int64_t p = (int64_t)t * k;
+      const hipError_t err = launch_combine_fp8(
+          y, y_stride, capacity_rows, y_scales, ids + p, expand_idx + p, send, scales + p,
+          shared ? static_cast<const uint16_t*>(shared) + t * shared_stride : nullptr,
+          shared_stride, bs - t < most ? bs - t : most, hidden, k, num_experts,
+          static_cast<uint16_t*>(out) + (int64_t)t * hidden, status, stream);
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+  }
   const dim3 grid((uint32_t)(bs * nchunks));
   const u32x4* yv = static_cast<const u32x4*>(y);
   const u32x4* sv = static_cast<const u32x4*>(shared);

@@ -290,6 +290,21 @@ static_assert((kCachedRowsPerCu + 1) * kCachedRowsLdsInts * 4 > 163840, "cap");
 constexpr int kUncachedPerCu = MOE_UNCACHED_PER_CU;
 constexpr int kUncachedLdsInts = lds_ints_for(kUncachedPerCu);
 
+// Tokens of one launch, at most `most`: whole ranking workgroups of deferred
+// ranks (which hold a 256th of a batch that large).
+int32_t tokens_a_launch(int32_t most, const DeferredRanks& dr) {
+  return dr.base ? most / dr.tokens_per_block * dr.tokens_per_block : most;
+}
+
+// Deferred ranks as a launch that begins with token t sees them.
+DeferredRanks ranks_from(DeferredRanks dr, int32_t t, int32_t k, int32_t num_experts) {
+  if (dr.base) {
+    dr.base += (int64_t)(t / dr.tokens_per_block) * num_experts;
+    dr.expand_idx += (int64_t)t * k;
+  }
+  return dr;
+}
+
 }  // namespace
 
 hipError_t launch_dispatch_bf16(const void* x, int64_t x_stride, int32_t bs, int32_t hidden,
@@ -299,7 +314,21 @@ hipError_t launch_dispatch_bf16(const void* x, int64_t x_stride, int32_t bs, int
                                 int32_t* status, hipStream_t stream, bool rows_cached,
                                 const DeferredRanks& dr) {
   constexpr int kT = MOE_DISPATCH_THREADS;
-  const int64_t items = (int64_t)bs * ((hidden / 8 + kT - 1) / kT);
+  const int32_t chunks = (hidden / 8 + kT - 1) / kT;
+  // Rows that were read ahead are too few for that.
+  const int32_t most = tokens_a_launch(most_items(kT) / chunks, dr);
+  if (bs > most && !rows_cached) {
+    for (int32_t t = 0; t < bs; t += most) {
+      const hipError_t err = launch_dispatch_bf16(
+          static_cast<const uint16_t*>(x) + t * x_stride, x_stride, bs - t < most ? bs - t : most,
+          hidden, ids + (int64_t)t * k, expand_idx + (int64_t)t * k, send, k, num_experts,
+          expand_x, expand_x_stride, capacity_rows, status, stream, false,
+          ranks_from(dr, t, k, num_experts));
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+  }
+  const int64_t items = (int64_t)bs * chunks;
   const bool big = items >= kSerialMinItems;
 #define MOE_SHAPE(TH, LDS, DEF, ORD)                                                      \
   return launch_bf16_shape<TH, LDS, DEF, ORD>(x, x_stride, bs, hidden, ids, expand_idx,   \
@@ -327,6 +356,19 @@ hipError_t launch_dispatch_fp8(const void* x, int64_t x_stride, int32_t bs, int3
                                void* expand_x, int64_t expand_x_stride, int64_t capacity_rows,
                                float* quant_scales, int32_t* status, hipStream_t stream,
                                const DeferredRanks& dr) {
+  constexpr int kT = MOE_FP8_THREADS;
+  const int32_t most = tokens_a_launch(most_items(kT) / ((hidden / 16 + kT - 1) / kT), dr);
+  if (bs > most) {
+    for (int32_t t = 0; t < bs; t += most) {
+      const hipError_t err = launch_dispatch_fp8(
+          static_cast<const uint16_t*>(x) + t * x_stride, x_stride, bs - t < most ? bs - t : most,
+          hidden, ids + (int64_t)t * k, expand_idx + (int64_t)t * k, send, k, num_experts,
+          expand_x, expand_x_stride, capacity_rows, quant_scales, status, stream,
+          ranks_from(dr, t, k, num_experts));
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+  }
   if (dr.base)
     return launch_fp8_shape<true>(x, x_stride, bs, hidden, ids, expand_idx, send, k,
                                   num_experts, expand_x, expand_x_stride, capacity_rows,

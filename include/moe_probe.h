@@ -64,8 +64,9 @@ int moe_probe_stream_mix(const void* src, int64_t src_rows_total, void* dst,
  * read-ahead of the token rows, then the scatter) for bf16 output from
  * contiguous rows of 32 to 240 MB; moe_dispatch_fused one (fused kernel, bs*k <= 2048) or two (the
  * layout's ranking launch, then the scatter); moe_combine, moe_combine_fp8,
- * the experts' products and the gradients one.  moe_combine and the gradients
- * take several beyond 2^24 items, of a pair or 1024 channels of a token each.
+ * the experts' products and the gradients one.  A scatter, combine or
+ * gradient whose threads would pass 2^31 (2^24 tokens of 1024 channels) takes
+ * several.
  * Calls that return an error or have nothing to do launch nothing and leave
  * the pairs bound.
  *
