@@ -55,6 +55,28 @@ bool row_ok(const void* base, int64_t stride, int32_t hidden, int elem) {
   return true;
 }
 
+// `rows` rows of `width` bytes, `stride` bytes apart.
+struct Bytes {
+  const void* base;
+  int64_t stride, width, rows;
+};
+
+Bytes flat(const void* base, int64_t bytes) { return {base, bytes, bytes, 1}; }
+
+// Whether two buffers share a byte.  Columns of one wider buffer (equal
+// strides) may lie side by side; with other strides the extents decide.
+bool overlap(const Bytes& a, const Bytes& b) {
+  if (a.base == nullptr || b.base == nullptr || a.rows == 0 || b.rows == 0) return false;
+  const int64_t at = reinterpret_cast<intptr_t>(a.base), bt = reinterpret_cast<intptr_t>(b.base);
+  const auto end = [](int64_t from, const Bytes& x) {  // any row count and stride
+    return (__int128)from + (__int128)(x.rows - 1) * x.stride + x.width;
+  };
+  if (end(at, a) <= bt || end(bt, b) <= at) return false;
+  if (a.stride != b.stride) return true;
+  const int64_t d = ((bt - at) % a.stride + a.stride) % a.stride;
+  return d < a.width || d + b.width > a.stride;
+}
+
 // Work items of the streaming kernels are indexed in 32 bits.
 bool rows_fit(int32_t bs, int32_t hidden) { return (int64_t)bs * (hidden / 8) <= INT32_MAX; }
 
@@ -159,10 +181,25 @@ int product_call(const moe::GroupedGemm& g, void* stream) {
   if (!row_ok(g.x, g.x_stride, g.in_features, 1)) return MOE_ERR_INVALID_ARG;
   if (g.x_stride > moe::kMaxProductStride) return MOE_ERR_INVALID_ARG;
   if (!row_ok(g.out, g.out_stride, g.out_features, g.gated ? 1 : 2)) return MOE_ERR_INVALID_ARG;
-  if (g.out == g.x) return MOE_ERR_INVALID_ARG;
   if (g.w == nullptr || !aligned16(g.w)) return MOE_ERR_INVALID_ARG;
   if (!aligned4(g.x_scales) || !aligned4(g.w_scales)) return MOE_ERR_INVALID_ARG;
   if (g.gated && !aligned4(g.out_scales)) return MOE_ERR_INVALID_ARG;
+  // Column tiles write a row while others still read it.
+  const int64_t cap = g.capacity_rows, elem = g.gated ? 1 : 2, in_blocks = g.in_features / 128;
+  const int64_t n = (int64_t)g.out_features * rows_per_expert;
+  const Bytes outs[] = {
+      {g.out, g.out_stride * elem, g.out_features * elem, cap},
+      flat(g.gated ? g.out_scales : nullptr, cap * (g.out_features / 128) * 4)};
+  const Bytes ins[] = {{g.x, g.x_stride, g.in_features, cap},
+                       flat(g.x_scales, cap * in_blocks * 4),
+                       flat(g.w, g.num_experts * n * g.in_features),
+                       flat(g.w_scales, g.num_experts * ((n + 127) / 128) * in_blocks * 4),
+                       flat(g.counts, g.num_experts * 4),
+                       flat(g.send, (g.num_experts + 1) * 4)};
+  if (overlap(outs[0], outs[1])) return MOE_ERR_INVALID_ARG;
+  for (const Bytes& o : outs)
+    for (const Bytes& i : ins)
+      if (overlap(o, i)) return MOE_ERR_INVALID_ARG;
   moe::GroupedGemm call = g;
   if (call.expected_rows == 0 || call.expected_rows > g.capacity_rows)
     call.expected_rows = g.capacity_rows;

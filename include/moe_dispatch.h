@@ -460,8 +460,9 @@ int moe_dispatch_fused_replicated(const void* x, int64_t x_stride, int32_t bs, i
  *                     chooses launch and tile shapes, never the result.
  *  out            out bf16 [capacity_rows, out_features], row stride
  *                     out_stride elements, 16-byte aligned, stride*2 % 16 ==
- *                     0; must not overlap an input (expand_x's own address
- *                     is refused).
+ *                     0; a buffer that overlaps an input is refused (columns
+ *                     of one wider buffer, at one stride, may lie side by
+ *                     side).
  *  status         in/out int32 [1] or NULL: MOE_FLAG_GUARD is OR-ed in when
  *                     a segment leaves [0, capacity_rows) (the rows outside
  *                     are skipped) or two segments share a row of the buffer
@@ -499,6 +500,8 @@ int moe_grouped_gemm_fp8(const void* expand_x, int64_t expand_x_stride, int64_t 
  *                     stride out_stride bytes, a multiple of 16; 16-byte
  *                     aligned.
  *  out_scales     out fp32 [capacity_rows, inter_features/128] row-major.
+ *                     Neither output may overlap the other or an input
+ *                     (quant_scales among them): such calls are refused.
  *  other arguments as for moe_grouped_gemm_fp8.
  */
 int moe_grouped_gemm_silu_fp8(const void* expand_x, int64_t expand_x_stride,
