@@ -855,7 +855,8 @@ def moe_combine_backward(grad_out: torch.Tensor, expand_x: Optional[torch.Tensor
     gradient is grad_out itself.  grad_expand_x [cap, H] bf16 holds
     expert_scales[t,j] * grad_out[t] at each pair's row (rows of no pair are
     not written; pass expand_x itself to overwrite it), grad_expert_scales
-    [BS, K] fp32 the dot products.  An output not needed is None; without
+    [BS, K] fp32 the dot products (pass expert_scales itself to overwrite it).
+    An output not needed is None; without
     need_scales expand_x may be None (then capacity_rows or grad_expand_x
     gives the rows)."""
     dev = _need(grad_out, torch.bfloat16, "grad_out", contiguous=False)

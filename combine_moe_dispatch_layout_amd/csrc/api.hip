@@ -515,6 +515,28 @@ int moe_combine_backward(const void* grad_out, int64_t grad_out_stride, const vo
     if (capacity_rows > 0 && !row_ok(expand_x, expand_x_stride, hidden, 2))
       return MOE_ERR_INVALID_ARG;
   }
+  // A pair's workgroup writes while others read; only what a pair alone reads
+  // (its row, its weight) may be overwritten by what it writes there.
+  const int64_t pairs = (int64_t)bs * k, width = (int64_t)hidden * 2;
+  const Bytes dy = {grad_expand_x, grad_expand_x_stride * 2, width, capacity_rows};
+  const Bytes dw = flat(grad_expert_scales, pairs * 4);
+  const Bytes ins[] = {{grad_out, grad_out_stride * 2, width, bs},
+                       flat(expert_ids, pairs * 4),
+                       flat(expand_idx, pairs * 4),
+                       flat(ep_send_counts, ((int64_t)num_experts + 1) * 4)};
+  for (const Bytes& i : ins)
+    if (overlap(dy, i) || overlap(dw, i)) return MOE_ERR_INVALID_ARG;
+  if (overlap(dy, dw)) return MOE_ERR_INVALID_ARG;
+  if (grad_expert_scales != nullptr) {
+    const Bytes y = {expand_x, expand_x_stride * 2, width, capacity_rows};
+    const bool in_place = grad_expand_x == expand_x && grad_expand_x_stride == expand_x_stride;
+    if (overlap(dw, y) || (!in_place && overlap(dy, y))) return MOE_ERR_INVALID_ARG;
+  }
+  if (grad_expand_x != nullptr) {
+    const Bytes w = flat(expert_scales, pairs * 4);
+    if (overlap(dy, w) || (grad_expert_scales != expert_scales && overlap(dw, w)))
+      return MOE_ERR_INVALID_ARG;
+  }
   return hip_status(moe::launch_combine_backward(
       grad_out, grad_out_stride, expand_x, expand_x_stride, capacity_rows, expert_ids, expand_idx,
       ep_send_counts, expert_scales, bs, hidden, k, num_experts, grad_expand_x,
@@ -535,10 +557,18 @@ int moe_dispatch_backward(const void* grad_expand_x, int64_t grad_expand_x_strid
     return MOE_ERR_INVALID_ARG;
   if (capacity_rows > 0 && !row_ok(grad_expand_x, grad_expand_x_stride, hidden, 2))
     return MOE_ERR_INVALID_ARG;
-  if (grad_x_add != nullptr &&
-      (grad_x_add == grad_x || !row_ok(grad_x_add, grad_x_add_stride, hidden, 2)))
+  if (grad_x_add != nullptr && !row_ok(grad_x_add, grad_x_add_stride, hidden, 2))
     return MOE_ERR_INVALID_ARG;
   if (!row_ok(grad_x, hidden, hidden, 2)) return MOE_ERR_INVALID_ARG;
+  const int64_t pairs = (int64_t)bs * k, width = (int64_t)hidden * 2;
+  const Bytes out = flat(grad_x, bs * width);
+  const Bytes ins[] = {{grad_expand_x, grad_expand_x_stride * 2, width, capacity_rows},
+                       {grad_x_add, grad_x_add_stride * 2, width, bs},
+                       flat(expert_ids, pairs * 4),
+                       flat(expand_idx, pairs * 4),
+                       flat(ep_send_counts, ((int64_t)num_experts + 1) * 4)};
+  for (const Bytes& i : ins)
+    if (overlap(out, i)) return MOE_ERR_INVALID_ARG;
   return hip_status(moe::launch_combine(grad_expand_x, grad_expand_x_stride, capacity_rows,
                                         expert_ids, expand_idx, ep_send_counts, nullptr,
                                         grad_x_add, grad_x_add_stride, bs, hidden, k,

@@ -49,8 +49,8 @@ __device__ __forceinline__ void add_products(const u32x4& g, const u32x4& y, flo
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     const u32x4* __restrict__ g, int64_t gs, const u32x4* y, int64_t ys, int64_t cap,
     const int32_t* __restrict__ ids, const int32_t* __restrict__ idx,
-    const int32_t* __restrict__ send, const float* __restrict__ scales, int32_t nvec, int32_t k,
-    int32_t E, u32x4* dy, int64_t dys, float* __restrict__ dw, int32_t* status) {
+    const int32_t* __restrict__ send, const float* scales, int32_t nvec, int32_t k,
+    int32_t E, u32x4* dy, int64_t dys, float* dw, int32_t* status) {
   constexpr int UNROLL = 4;
   __shared__ int send_lds[StagedSend<kThreads>::kSlots];
   __shared__ float sum_lds[kThreads / kWave];
@@ -117,8 +117,8 @@ template <int GROUP, int VECS, int PAIRS>
 __global__ __launch_bounds__(kShortThreads) void combine_backward_short_kernel(
     const u32x4* __restrict__ g, int64_t gs, const u32x4* y, int64_t ys, int64_t cap,
     const int32_t* __restrict__ ids, const int32_t* __restrict__ idx,
-    const int32_t* __restrict__ send, const float* __restrict__ scales, int32_t nvec, int32_t k,
-    int32_t pairs, int32_t E, u32x4* dy, int64_t dys, float* __restrict__ dw, int32_t* status) {
+    const int32_t* __restrict__ send, const float* scales, int32_t nvec, int32_t k,
+    int32_t pairs, int32_t E, u32x4* dy, int64_t dys, float* dw, int32_t* status) {
   constexpr int kGroups = kShortThreads / GROUP;
   const int lane = threadIdx.x % GROUP;
   const int32_t first = blockIdx.x * (kGroups * PAIRS) + threadIdx.x / GROUP;

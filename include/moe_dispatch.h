@@ -535,9 +535,11 @@ int moe_grouped_gemm_silu_fp8(const void* expand_x, int64_t expand_x_stride,
  *                     be expand_x itself (same address and stride): each
  *                     element is read before it is overwritten.
  *  grad_expert_scales
- *                 out fp32 [bs, k] row-major, or NULL: not wanted.  One of
- *                     the two outputs must be given (unless capacity_rows
- *                     is 0).
+ *                 out fp32 [bs, k] row-major, or NULL: not wanted.  May be
+ *                     expert_scales itself.  One of the two outputs must be
+ *                     given (unless capacity_rows is 0).  An output that
+ *                     overlaps the other or what is read, except as named
+ *                     here, is refused.
  *  status         in/out int32 [1] or NULL, as for moe_combine.
  */
 int moe_combine_backward(const void* grad_out, int64_t grad_out_stride, const void* expand_x,
@@ -560,9 +562,9 @@ int moe_combine_backward(const void* grad_out, int64_t grad_out_stride, const vo
  * or 0.  (e4m3 dispatch: the quantisation counts as the identity.)
  *
  *  grad_expand_x  in  bf16 [capacity_rows, hidden].
- *  grad_x_add     in  bf16 [bs, hidden], row stride grad_x_add_stride, or NULL;
- *                     must not overlap grad_x (grad_x itself is refused).
- *  grad_x         out bf16 [bs, hidden], contiguous.
+ *  grad_x_add     in  bf16 [bs, hidden], row stride grad_x_add_stride, or NULL.
+ *  grad_x         out bf16 [bs, hidden], contiguous; one that overlaps an
+ *                     input is refused.
  *  other arguments as for moe_combine.
  */
 int moe_dispatch_backward(const void* grad_expand_x, int64_t grad_expand_x_stride,

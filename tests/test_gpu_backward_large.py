@@ -91,3 +91,24 @@ def test_dispatch_backward_and_combine_beyond_one_launch(moe, bs, hidden, k):
             assert torch.equal(out[t], want.bfloat16()), t
             out[t] = 0
         assert not out.any()
+
+
+@pytest.mark.parametrize("bs,hidden", [(300, 64), (300, 512), (3000, 512), (3000, 1024), (70, 2080)])
+def test_weights_overwritten_by_their_gradient(moe, bs, hidden):
+    """grad_expert_scales may be expert_scales: a pair's weight is read before
+    its gradient is written, whatever threads a pair has."""
+    k, e = 4, 12
+    gen = torch.Generator().manual_seed(bs + hidden)
+    ids = torch.rand((bs, e), generator=gen).topk(k, 1).indices.int().to(DEV)
+    lay = moe.moe_dispatch_layout(ids, e)
+    cap = moe.moe_dispatch_capacity(bs, k, e)
+    y = torch.randn((cap, hidden), generator=gen).to(DEV, torch.bfloat16)
+    g = torch.randn((bs, hidden), generator=gen).to(DEV, torch.bfloat16)
+    w = torch.rand((bs, k), generator=gen).to(DEV)
+    route = (ids, lay.expand_idx, lay.ep_send_counts)
+    rows = [torch.zeros((cap, hidden), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    dy, dw = moe.moe_combine_backward(g, y, *route, w, e, grad_expand_x=rows[0])
+    dy2, dw2 = moe.moe_combine_backward(g, y, *route, w, e, grad_expand_x=rows[1],
+                                        grad_expert_scales=w)
+    assert dw2.data_ptr() == w.data_ptr()
+    assert torch.equal(dw2, dw) and torch.equal(dy2, dy)
