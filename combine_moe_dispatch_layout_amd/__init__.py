@@ -74,7 +74,8 @@ __all__ = [
     "moe_dispatch_fused_noalloc", "moe_noalloc_scratch_bytes",
     "moe_grouped_gemm_fp8", "moe_grouped_gemm_silu_fp8", "moe_combine_backward",
     "moe_dispatch_backward", "moe_plan_compensation",
-    "moe_combine_fp8", "moe_probe_stream_mix", "moe_probe_empty", "moe_time_next_launches",
+    "moe_combine_fp8", "moe_probe_stream_mix", "moe_probe_empty", "moe_probe_product_tile",
+    "moe_time_next_launches",
     "moe_time_unused_launches", "prepare", "Prepared",
     "MOE_BF16", "MOE_FP8_E4M3", "MOE_FLAG_ID_RANGE", "MOE_FLAG_DUP_ID", "MOE_FLAG_GUARD",
 ]
@@ -142,6 +143,7 @@ def load_library() -> ctypes.CDLL:
                                                   sz, P]),
         "moe_probe_stream_mix": (ctypes.c_int, [P, i64, P, i64, i32, i32, i32, i32, P, P, P]),
         "moe_probe_empty": (ctypes.c_int, [i32, P]),
+        "moe_probe_product_tile": (ctypes.c_int, [i32, i32, i64, i32, i32, i64, P, P, P]),
         "moe_time_next_launches": (ctypes.c_int, [P, P, i32]),
         "moe_time_unused_launches": (i32, []),
         "moe_dispatch_layout_replicated": (ctypes.c_int, [P, i32, i32, i32, P, P, i32,
@@ -856,9 +858,8 @@ def moe_combine_backward(grad_out: torch.Tensor, expand_x: Optional[torch.Tensor
     expert_scales[t,j] * grad_out[t] at each pair's row (rows of no pair are
     not written; pass expand_x itself to overwrite it), grad_expert_scales
     [BS, K] fp32 the dot products (pass expert_scales itself to overwrite it).
-    An output not needed is None; without
-    need_scales expand_x may be None (then capacity_rows or grad_expand_x
-    gives the rows)."""
+    An output not needed is None; without need_scales expand_x may be None
+    (then capacity_rows or grad_expand_x gives the rows)."""
     dev = _need(grad_out, torch.bfloat16, "grad_out", contiguous=False)
     if grad_out.dim() != 2:
         raise ValueError("grad_out must be [BS, H]")
@@ -1105,6 +1106,19 @@ def moe_probe_empty(workgroups: int, device: Optional[int] = None) -> None:
     stream = _raw_stream(dev) if _raw_stream is not None else \
         torch.cuda.current_stream(dev).cuda_stream
     _check(load_library().moe_probe_empty(workgroups, stream))
+
+
+def moe_probe_product_tile(capacity_rows: int, num_experts: int, out_features: int, *,
+                           expected_rows: int = 0, gated: bool = False,
+                           grouped: bool = True) -> "tuple[int, int, bool]":
+    """The tile an experts' product of these sizes takes (include/moe_probe.h):
+    (token rows, output channels, weights' loads marked as read once).
+    out_features is I for the gated form; grouped: with expert_counts."""
+    out = [ctypes.c_int32() for _ in range(3)]
+    _check(load_library().moe_probe_product_tile(
+        int(gated), int(grouped), capacity_rows, num_experts, out_features, expected_rows,
+        *map(ctypes.byref, out)))
+    return out[0].value, out[1].value, bool(out[2].value)
 
 
 def moe_time_next_launches(pairs) -> None:

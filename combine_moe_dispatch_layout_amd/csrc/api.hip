@@ -161,22 +161,35 @@ int layout_then_scatter(const void* x, int64_t x_stride, int32_t bs, int32_t hid
                                              quant_scales, status, s, dr));
 }
 
-// Rules of the experts' products, and their launch.  Either both of counts
+// Rules of the experts' products' sizes.
+bool product_sizes_ok(const moe::GroupedGemm& g) {
+  const int32_t rows_per_expert = g.gated ? 2 : 1;
+  if (g.num_experts < 1 || g.num_experts > moe::kMaxExperts) return false;
+  if (g.in_features <= 0 || g.in_features % 128 != 0 || g.in_features > 65536)
+    return false;
+  if (g.out_features <= 0 || g.out_features % (g.gated ? 128 : 32) != 0 ||
+      g.out_features > 65536 / rows_per_expert)
+    return false;
+  if (g.capacity_rows < 0 || g.capacity_rows > moe::kMaxRows || g.expected_rows < 0)
+    return false;
+  // Tiles are counted in 32 bits.
+  if (g.capacity_rows > (int64_t(1) << 40) / g.out_features) return false;
+  return true;
+}
+
+// Unknown rows: all that fit.
+moe::GroupedGemm with_expected_rows(moe::GroupedGemm g) {
+  if (g.expected_rows == 0 || g.expected_rows > g.capacity_rows) g.expected_rows = g.capacity_rows;
+  return g;
+}
+
+// All rules of the experts' products, and their launch.  Either both of counts
 // and send are given, or neither (one group of all rows).
 int product_call(const moe::GroupedGemm& g, void* stream) {
   const int32_t rows_per_expert = g.gated ? 2 : 1;
-  if (g.num_experts < 1 || g.num_experts > moe::kMaxExperts) return MOE_ERR_INVALID_ARG;
+  if (!product_sizes_ok(g)) return MOE_ERR_INVALID_ARG;
   if ((g.counts == nullptr) != (g.send == nullptr)) return MOE_ERR_INVALID_ARG;
   if (g.counts == nullptr && g.num_experts != 1) return MOE_ERR_INVALID_ARG;
-  if (g.in_features <= 0 || g.in_features % 128 != 0 || g.in_features > 65536)
-    return MOE_ERR_INVALID_ARG;
-  if (g.out_features <= 0 || g.out_features % (g.gated ? 128 : 32) != 0 ||
-      g.out_features > 65536 / rows_per_expert)
-    return MOE_ERR_INVALID_ARG;
-  if (g.capacity_rows < 0 || g.capacity_rows > moe::kMaxRows || g.expected_rows < 0)
-    return MOE_ERR_INVALID_ARG;
-  // Tiles are counted in 32 bits.
-  if (g.capacity_rows > (int64_t(1) << 40) / g.out_features) return MOE_ERR_INVALID_ARG;
   if (g.capacity_rows == 0) return MOE_OK;
   if (!row_ok(g.x, g.x_stride, g.in_features, 1)) return MOE_ERR_INVALID_ARG;
   if (g.x_stride > moe::kMaxProductStride) return MOE_ERR_INVALID_ARG;
@@ -200,10 +213,8 @@ int product_call(const moe::GroupedGemm& g, void* stream) {
   for (const Bytes& o : outs)
     for (const Bytes& i : ins)
       if (overlap(o, i)) return MOE_ERR_INVALID_ARG;
-  moe::GroupedGemm call = g;
-  if (call.expected_rows == 0 || call.expected_rows > g.capacity_rows)
-    call.expected_rows = g.capacity_rows;
-  return hip_status(moe::launch_grouped_gemm(call, static_cast<hipStream_t>(stream)));
+  return hip_status(
+      moe::launch_grouped_gemm(with_expected_rows(g), static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace
@@ -627,6 +638,29 @@ int moe_grouped_gemm_silu_fp8(const void* expand_x, int64_t expand_x_stride,
   g.out_scales = out_scales;
   g.status = status;
   return product_call(g, stream);
+}
+
+int moe_probe_product_tile(int32_t gated, int32_t grouped, int64_t capacity_rows,
+                           int32_t num_experts, int32_t out_features, int64_t expected_rows,
+                           int32_t* tile_rows, int32_t* tile_cols, int32_t* weights_once) {
+  static const int32_t some = 0;
+  moe::GroupedGemm g;
+  g.capacity_rows = capacity_rows;
+  g.num_experts = num_experts;
+  g.in_features = 128;  // no rule looks at it
+  g.out_features = out_features;
+  g.expected_rows = expected_rows;
+  g.gated = gated != 0;
+  g.counts = grouped ? &some : nullptr;
+  if (!product_sizes_ok(g) || capacity_rows == 0 || (!grouped && num_experts != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (tile_rows == nullptr || tile_cols == nullptr || weights_once == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  const moe::ProductTile t = moe::grouped_gemm_tile(with_expected_rows(g));
+  *tile_rows = t.rows;
+  *tile_cols = t.cols;
+  *weights_once = t.once;
+  return MOE_OK;
 }
 
 int moe_time_next_launches(void* const* start_events, void* const* stop_events, int32_t n) {

@@ -846,23 +846,24 @@ hipError_t launch_shape(const ProductArgs& p, int64_t expected_rows, hipStream_t
 // Where the small tiles all run at once they are the quickest whatever the rows
 // (4 experts of 225 rows, gated 2048 -> 1024: 21 us, 64-row tiles 24, 128-row
 // 35; one of 1024, plain 2048 -> 2048: 14.8, 15.8 and 21), then those of 64.
-hipError_t launch_gated(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
+template <class Use>
+auto with_gated_shape(const ProductArgs& p, int64_t expected_rows, Use use) {
   using Large = Shape<true, 2, 2, 2, 4, 3, false>;
   using Middle = Shape<true, 1, 2, 2, 4, 3, false>;
   using MiddleOnce = Shape<true, 1, 2, 2, 4, 3, true>;
   using Small = Shape<true, 1, 2, 1, 4, 4, false>;
   using SmallOnce = Shape<true, 1, 2, 1, 4, 4, true>;
   const int64_t rows = expected_rows / p.E;
-  if (rows <= 20) return launch_shape<SmallOnce>(p, expected_rows, stream);
-  if (tiles_to_expect<Small>(p, expected_rows) <= kComputeUnits)
-    return launch_shape<Small>(p, expected_rows, stream);
-  if (rows <= 44) return launch_shape<MiddleOnce>(p, expected_rows, stream);
+  if (rows <= 20) return use(SmallOnce{});
+  if (tiles_to_expect<Small>(p, expected_rows) <= kComputeUnits) return use(Small{});
+  if (rows <= 44) return use(MiddleOnce{});
   if (rows <= 96 || tiles_to_expect<Middle>(p, expected_rows) <= kComputeUnits)
-    return launch_shape<Middle>(p, expected_rows, stream);
-  return launch_shape<Large>(p, expected_rows, stream);
+    return use(Middle{});
+  return use(Large{});
 }
 
-hipError_t launch_plain(const ProductArgs& p, int64_t expected_rows, hipStream_t stream) {
+template <class Use>
+auto with_plain_shape(const ProductArgs& p, int64_t expected_rows, Use use) {
   using Full = Shape<false, 4, 8, 4, 2, 2, false>;   // 256 x 256
   using Half = Shape<false, 4, 4, 2, 4, 3, false>;   // 128 x 256
   using Middle = Shape<false, 2, 4, 2, 4, 3, false>;
@@ -870,12 +871,12 @@ hipError_t launch_plain(const ProductArgs& p, int64_t expected_rows, hipStream_t
   using Small = Shape<false, 2, 2, 1, 4, 3, false>;  // two of them a compute unit
   using SmallOnce = Shape<false, 2, 2, 1, 4, 3, true>;
   const int64_t rows = expected_rows / p.E;
-  if (rows <= 16) return launch_shape<SmallOnce>(p, expected_rows, stream);
+  if (rows <= 16) return use(SmallOnce{});
   if (tiles_to_expect<Small>(p, expected_rows) <= 2 * kComputeUnits)
-    return launch_shape<Small>(p, expected_rows, stream);
-  if (rows <= 48) return launch_shape<MiddleOnce>(p, expected_rows, stream);
+    return use(Small{});
+  if (rows <= 48) return use(MiddleOnce{});
   if (tiles_to_expect<Middle>(p, expected_rows) <= kComputeUnits)
-    return launch_shape<Middle>(p, expected_rows, stream);
+    return use(Middle{});
   // A full tile takes 1.6 times a half one's time (its operands move less)
   // but leaves more of the last round idle: whichever's rounds are shorter.
   // 2048 -> 7168, half and full: 32 experts of 1024 rows 628 and 542 us, of 256
@@ -883,13 +884,17 @@ hipError_t launch_plain(const ProductArgs& p, int64_t expected_rows, hipStream_t
   const auto rounds = [](int64_t tiles) { return (tiles + kComputeUnits - 1) / kComputeUnits; };
   if (rounds(tiles_to_expect<Full>(p, expected_rows)) * 8 <
       rounds(tiles_to_expect<Half>(p, expected_rows)) * 5)
-    return launch_shape<Full>(p, expected_rows, stream);
-  return launch_shape<Half>(p, expected_rows, stream);
+    return use(Full{});
+  return use(Half{});
 }
 
-}  // namespace
+template <class Use>
+auto with_shape(const GroupedGemm& g, const ProductArgs& p, Use use) {
+  return g.gated ? with_gated_shape(p, g.expected_rows, use)
+                 : with_plain_shape(p, g.expected_rows, use);
+}
 
-hipError_t launch_grouped_gemm(const GroupedGemm& g, hipStream_t stream) {
+ProductArgs args_of(const GroupedGemm& g) {
   ProductArgs p;
   p.x = static_cast<const uint8_t*>(g.x);
   p.xs = g.x_stride;
@@ -907,8 +912,23 @@ hipError_t launch_grouped_gemm(const GroupedGemm& g, hipStream_t stream) {
   p.out_stride = g.out_stride;
   p.out_scales = g.out_scales;
   p.status = g.status;
-  return g.gated ? launch_gated(p, g.expected_rows, stream)
-                 : launch_plain(p, g.expected_rows, stream);
+  return p;
+}
+
+}  // namespace
+
+hipError_t launch_grouped_gemm(const GroupedGemm& g, hipStream_t stream) {
+  const ProductArgs p = args_of(g);
+  return with_shape(g, p, [&](auto shape) {
+    return launch_shape<decltype(shape)>(p, g.expected_rows, stream);
+  });
+}
+
+ProductTile grouped_gemm_tile(const GroupedGemm& g) {
+  return with_shape(g, args_of(g), [](auto shape) {
+    using S = decltype(shape);
+    return ProductTile{S::kRows, S::kCols, S::kOnce};
+  });
 }
 
 }  // namespace moe

@@ -470,5 +470,12 @@ struct GroupedGemm {
 // Row offsets inside a tile of at most 256 rows are 32-bit.
 constexpr int64_t kMaxProductStride = int64_t(1) << 23;
 hipError_t launch_grouped_gemm(const GroupedGemm& g, hipStream_t stream);
+// The tile it takes: token rows x output channels, and whether its weights'
+// loads are marked as read once.
+struct ProductTile {
+  int32_t rows, cols;
+  bool once;
+};
+ProductTile grouped_gemm_tile(const GroupedGemm& g);
 
 }  // namespace moe

@@ -8,7 +8,8 @@
  *    plain kernel of that shape reaches;
  *  - moe_time_next_launches binds HIP events to the library's next kernel
  *    launches, so each kernel is timed by its own start and end rather than
- *    by events recorded around it.
+ *    by events recorded around it;
+ *  - moe_probe_product_tile says which tile an experts' product takes.
  * Conventions (device pointers, stream as void*, status codes) are those of
  * moe_dispatch.h.
  */
@@ -93,6 +94,21 @@ int32_t moe_time_unused_launches(void);
  * launch fails, else 0.
  */
 int moe_probe_empty(int32_t workgroups, void* stream);
+
+/*
+ * The tile that moe_grouped_gemm_fp8 (gated 0) or moe_grouped_gemm_silu_fp8
+ * (gated 1) takes for a call of these sizes: token rows x output channels of
+ * one workgroup, and whether the weights' loads are marked as read once.
+ * Host code, no launch; results of the products do not depend on it.
+ *  grouped       in   1: with expert_counts, 0: without (num_experts 1).
+ *  out_features  in   out_features, or inter_features of the gated form.
+ *  others        in   as for the product.
+ * Returns MOE_ERR_INVALID_ARG (1) for sizes that the product refuses, no rows
+ * or a NULL output, else 0.
+ */
+int moe_probe_product_tile(int32_t gated, int32_t grouped, int64_t capacity_rows,
+                           int32_t num_experts, int32_t out_features, int64_t expected_rows,
+                           int32_t* tile_rows, int32_t* tile_cols, int32_t* weights_once);
 
 #ifdef __cplusplus
 }
