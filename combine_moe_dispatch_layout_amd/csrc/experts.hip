@@ -786,10 +786,12 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
   if (ahead < kStages - 1) wait_and_meet<0>();
   for (uint32_t tile = first_tile; tile < tiles; tile += gridDim.x) {
     const TileAt at = locate<S>(p, sh.map, tile, col_tiles);
-    // Where tiles are often half empty, waves without rows only load: 256
-    // experts of 32 rows, 7168 -> 2048 gated, 1404 -> 1237 us (of 64, where
-    // they seldom are, it costs 5 %); 2048 -> 7168, 43 rows: 817 -> 715.
-    const bool any = !(S::kOnce && S::WR > 1) || wr * RT * kSide < at.live;
+    // Gated, where tiles are often half empty, waves without rows only load:
+    // 256 experts of 20 to 32 rows, 7168 -> 2048, 8 to 14 % quicker (32 each:
+    // 1288 -> 1118 us), of 40 to 48 equal ones within 1 % and skewed ones 5 to
+    // 8 %; 64 experts, 4096 -> 1536, of 24 3 %, of 40 to 48 1 to 2 % slower.
+    // The plain product measures the same either way.
+    const bool any = !(kGated && S::kOnce && S::WR > 1) || wr * RT * kSide < at.live;
     for (int32_t b = 0; b < kb; ++b) {
       // This block's loads are done, everyone's (scale loads between them
       // only make the wait stricter), and the block before it is read: its
