@@ -8,9 +8,10 @@
 // Each row of y is read once and each row of dy written once; a token's pairs
 // run on one XCD, whose L2 gives them g.  Long rows have a workgroup a pair,
 // short ones (up to 1024 channels, or 2048 where the pairs are many) a group
-// of lanes.  HBM bounds both: 4096 tokens of 7168 channels, K = 8, take 182 to
-// 189 us (1.0 GB at 5.3 to 5.6 TB/s; a copy of 2 GiB reaches 5.0), 128 tokens
-// 8.9; 16384 tokens of 512 channels 54 us (0.55 GB).
+// of lanes.  Memory bounds both: 4096 tokens of 7168 channels, K = 8, take 182
+// to 192 us (1.0 GB at 5.2 to 5.5 TB/s; a copy of 2 GiB reaches 4.8 to 5.0), 128
+// tokens 8.9 to 9.3; 16384 tokens of 512 channels 54 to 59 us (0.285 GB at 4.8
+// to 5.3 TB/s).
 #include "moe_internal.h"
 
 namespace moe {
@@ -19,7 +20,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kShortThreads = 256;
 // Up to this many pairs every pair has a group of lanes (or a workgroup) of its
-// own; beyond, groups take two.
+// own; beyond, groups take two of rows of 264 to 2048 channels (shorter rows
+// keep a group a pair, longer ones a workgroup).
 constexpr int64_t kFewPairs = 4096;
 // Pairs of one launch (2^24), of at most a workgroup each: larger batches take
 // several.

@@ -14,20 +14,22 @@
 //
 // The plain product multiplies e4m3 in the matrix unit (16 x 16 x 128, a
 // block an instruction).  Its sums keep 13 bits below the largest of 8
-// products, which a bf16 output does not show; the gated form's fp32 scales
-// would (1.3e-5 off), so there the codes are widened, exactly, to fp16
-// (32 x 32 x 16; 1e-7) at 40 % of the rate.
+// products, which moves 2 % of the bf16 outputs by one step and leaves their
+// error against 64 bits as it is; the gated form's fp32 scales would show it
+// (1.3e-5 off), so there the codes are widened, exactly, to fp16 (32 x 32 x 16;
+// 1e-7) at 40 % of the rate.
 //
 // One workgroup a compute unit stays for the whole launch and walks tiles, so
 // that a tile's first loads are under way while the one before is finished.
 // Operands go from memory to a ring of stages in shared memory without
 // passing registers.  Few rows an expert: the weights' bytes bound it
-// (128 tokens on 256 experts, 2048 -> 7168: 574 us, 6.5 TB/s; gated 7168 ->
-// 2 * 2048: 1070 us, 6.9 TB/s; without the non-temporal mark 619 and 1214).
+// (128 tokens on 256 experts, 2048 -> 7168: 573 - 587 us, 6.4 TB/s; gated 7168 ->
+// 2 * 2048: 1070 - 1131 us, 6.5 - 6.9 TB/s; without the non-temporal mark 620
+// and 1214 - 1267).
 // Many: the matrix unit's power does, which lowers the clock to 1.9 - 2.1 GHz,
 // and what moving the operands adds to it (32 experts of 1024 rows, gated:
-// 1.87 - 1.97 ms, 1020 TFLOP/s; with operands from the first cache 1.60 ms at
-// 2.3 GHz; plain 2048 -> 7168: 542 us, 1775 TFLOP/s).  Between the two,
+// 1.81 - 2.01 ms, 960 - 1060 TFLOP/s; with operands from the first cache 1.60 ms
+// at 2.3 GHz; plain 2048 -> 7168: 505 - 542 us, 1775 - 1905 TFLOP/s).  Between the two,
 // 128 rows an expert on average, 0.94 - 1.0 ms is what 0.86 ms of loads and 0.74 ms
 // of products take together.
 #include <type_traits>
@@ -301,7 +303,8 @@ __device__ __forceinline__ uint32_t codes4(float h0, float h1, float h2, float h
 // The lane, counted again where it is asked for.  What is made of it is made
 // where it is needed, once a tile or a few blocks, and neither is kept in
 // registers through the products, which have none left (kept values were
-// spilled, and each wait for one drained the loads under way).
+// spilled, and each wait for one drained the loads under way; the gated 32- and
+// 64-row tiles still spill up to 5 scalar ones, to lanes of a vector register).
 __device__ __forceinline__ int lane_again() {
   int none = 0;
   __asm__ volatile("" : "+v"(none));  // new to the compiler
@@ -385,8 +388,9 @@ constexpr int kTurnBlocks = 7;  // and how much further on the next ones do
 // weight rows.  Gated, half of a wave's weight rows are gate rows and half
 // the up rows of the same channels.  STAGES blocks have a place in shared
 // memory: the one that is multiplied and those whose loads are under way.
-// ONCE: so few rows an expert that one row tile has them all, and its weights
-// are read once.
+// ONCE: so few rows an expert that one row tile has them all on average, and
+// most weights are read once.  (An expert with more reads its own again, from
+// beyond the caches that the mark passes by.)
 template <bool GATED_, int RT_, int CT_, int WR_, int WC_, int STAGES_, bool ONCE_>
 struct Shape {
   static constexpr bool kGated = GATED_, kOnce = ONCE_;
@@ -524,9 +528,10 @@ struct Loader {
     }
     // Weight rows a multiple of 4096 bytes apart share memory channels, and
     // tiles that run together would all ask the same few: there column tiles
-    // begin at different blocks and go round (64 experts of 8 rows, 4096
-    // channels: 181 -> 151 us gated, 117 -> 96 us plain; elsewhere it costs
-    // up to 4 %, tiles side by side no longer sharing the rows they read).
+    // begin at different blocks and go round (64 experts of 8 rows, 4096 ->
+    // 1536 gated 169 -> 131 us, 4096 -> 4096 plain 204 -> 169; of 64 rows 191 ->
+    // 158 and 249 -> 205; of 256 within 3 % either way; at other channel counts
+    // it costs up to 4 %, tiles side by side no longer sharing the rows they read).
     // The start depends on the output channel alone, so the sums of a row do
     // not depend on the tile's shape or the rows with it.
     turn = p.K % kTurnStride == 0 ? col0 / kTurnCols * kTurnBlocks % kb : 0;
@@ -836,18 +841,35 @@ hipError_t launch_shape(const ProductArgs& p, int64_t expected_rows, hipStream_t
 
 // Rows to expect of an expert choose the tile: few rows leave the weights'
 // bytes to count, many the squares.  Times in us of 64 experts by rows an
-// expert and tile:
-//   gated, 4096 -> 1536      8    16    24    32    48    64   128   187   256
-//               32 rows    132   133   155   172   223   267   439   586   798
-//               64 rows    150   153   152   153   175   225   339   447   566
-//              128 rows    207   211   219   215   228   228   327   424   510
-//   plain, 1536 -> 4096
-//               32 rows     64    71    80    99   129   145   231   330   435
-//               64 rows     66    72    74    77    85   107   149   182   221
-//              128 rows     89    79    81    83    88    92   117   139   175
+// expert on average and tile, for equal counts and (below) for counts that
+// fall with the expert's rank to the power -0.6:
+//   gated, 4096 -> 1536     8   16   24   32   44   64   96  128  187  256
+//          32 rows, once  126  127  128  130  203  203  291  374  537  705
+//                         145  141  140  165  194  252  343  441  599  786
+//                32 rows  142  143  144  144  214  214  306  400  564  717
+//                         160  156  150  171  196  261  367  461  629  826
+//          64 rows, once  126  128  129  130  148  153  275  275  374  492
+//                         128  145  153  162  175  212  275  357  467  599
+//                64 rows  145  146  146  147  150  153  267  282  386  502
+//                         146  176  168  166  168  207  267  336  451  563
+//               128 rows  206  202  200  200  208  210  212  220  405  415
+//                         204  190  223  230  243  257  270  316  399  506
+//   plain, 1536 -> 4096     8   16   24   32   44   64   96  128  187  256
+//          32 rows, once   65   68   72   75  130  110  171  191  302  393
+//                          68   75   90   91  119  150  192  236  338  451
+//                32 rows   77   78   78   79   97  103  127  163  218  294
+//                          77   82   86   88   98  110  140  169  230  297
+//          64 rows, once   67   70   72   75   78   82  135  113  162  193
+//                          67   74   78   83   86   98  127  163  188  227
+//                64 rows   76   78   77   79   84   89  106  113  154  196
+//                          76   80   82   85   87   96  109  132  167  209
+//               128 rows   77   78   78   81   86   90   97  102  131  145
+//                          77   77   86   88   93   95  100  113  134  165
+// The mean alone decides: a batch's skew is not known on the host.  At 96 equal
+// rows the gated 128-row tile would be the quicker, at 96 skewed ones the same.
 // Where the small tiles all run at once they are the quickest whatever the rows
-// (4 experts of 225 rows, gated 2048 -> 1024: 21 us, 64-row tiles 24, 128-row
-// 35; one of 1024, plain 2048 -> 2048: 14.8, 15.8 and 21), then those of 64.
+// (4 experts of 225 rows, gated 2048 -> 1024: 21.6 us, 64-row tiles 24.9, 128-row
+// 34.5; one of 1024, plain 2048 -> 2048: 15.1, 16.6 and 21.3), then those of 64.
 template <class Use>
 auto with_gated_shape(const ProductArgs& p, int64_t expected_rows, Use use) {
   using Large = Shape<true, 2, 2, 2, 4, 3, false>;
@@ -881,8 +903,9 @@ auto with_plain_shape(const ProductArgs& p, int64_t expected_rows, Use use) {
     return use(Middle{});
   // A full tile takes 1.6 times a half one's time (its operands move less)
   // but leaves more of the last round idle: whichever's rounds are shorter.
-  // 2048 -> 7168, half and full: 32 experts of 1024 rows 628 and 542 us, of 256
-  // 207 and 210; one of 8192 142 and 135; 1408 -> 4224, one of 5000 49 and 52.
+  // 2048 -> 7168, half and full: 32 experts of 1024 rows 599 and 505 us, of 256
+  // 168 and 167; one of 8192 148 and 137, of 4096 84 and 70; 1408 -> 4224, one of
+  // 5000 47 and 51.
   const auto rounds = [](int64_t tiles) { return (tiles + kComputeUnits - 1) / kComputeUnits; };
   if (rounds(tiles_to_expect<Full>(p, expected_rows)) * 8 <
       rounds(tiles_to_expect<Half>(p, expected_rows)) * 5)
