@@ -66,6 +66,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -73,11 +74,6 @@ import numpy as np
 from typing import NamedTuple, Optional
 
 import torch
-
-try:  # csrc/binding.cpp; load_library() says so if it is not built
-    from . import _binding
-except ImportError:
-    _binding = None
 
 __all__ = [
     "MoeError", "MoeStatusError", "Layout", "library_path", "load_library",
@@ -119,6 +115,27 @@ class MoeError(RuntimeError):
 
 def library_path() -> str:
     return _LIB_PATH
+
+
+def _extension():
+    """The binding's extension (csrc/binding.cpp).  It is looked up where it is
+    needed, not when the package is imported: a build that imports the package
+    makes it afterwards."""
+    name = __name__ + "._binding"
+    importlib.invalidate_caches()
+    try:
+        return importlib.import_module(name)
+    except ModuleNotFoundError as e:
+        if e.name != name:
+            raise
+        raise ImportError("the binding's extension (csrc/binding.cpp) is missing: build it with "
+                          "`python -m combine_moe_dispatch_layout_amd.build`") from None
+
+
+def __getattr__(name: str):
+    if name == "_binding":  # before its import has made it an attribute
+        return _extension()
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def load_library() -> ctypes.CDLL:
@@ -192,12 +209,10 @@ def load_library() -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    if _binding is None:
-        raise ImportError("the binding's extension (csrc/binding.cpp) is missing: build it with "
-                          "`python -m combine_moe_dispatch_layout_amd.build`")
+    binding = _extension()
     for name in _FAST_CALLS:  # the same functions, called without ctypes
-        _binding.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
-        setattr(lib, name, getattr(_binding, name))
+        binding.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
+        setattr(lib, name, getattr(binding, name))
     _lib = lib
     return lib
 
@@ -1015,17 +1030,25 @@ _NORM_OUT = {"bf16": (True, False), "fp8": (False, True), "e4m3": (False, True),
 _BF16, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
 
 
-def _not_built(*args):
-    load_library()  # says so
-    raise ImportError("the binding's extension is not built")
+# The extension's functions, each of which takes all four from it when it is
+# first called.
+def _on_first_call(name: str):
+    def first_call(*args):
+        global _new_at, _matrix_facts, _rows_facts, _flat_facts
+        binding = _extension()
+        _new_at, _matrix_facts = binding.new, binding.matrix
+        _rows_facts, _flat_facts = binding.rows, binding.flat
+        return getattr(binding, name)(*args)
+
+    return first_call
 
 
 # A new contiguous tensor beside another, of a dtype and one or two sizes, with
 # its address.
-_new_at = _binding.new if _binding else _not_built
-_matrix_facts = _binding.matrix if _binding else _not_built
-_rows_facts = _binding.rows if _binding else _not_built
-_flat_facts = _binding.flat if _binding else _not_built
+_new_at = _on_first_call("new")
+_matrix_facts = _on_first_call("matrix")
+_rows_facts = _on_first_call("rows")
+_flat_facts = _on_first_call("flat")
 
 
 def _matrix(t, dtype, name: str):
