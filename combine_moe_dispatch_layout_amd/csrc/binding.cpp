@@ -160,10 +160,10 @@ Entry entries[] = {{"moe_rms_norm", nullptr},      {"moe_rms_norm_backward", nul
 template <int WHICH, typename... A, size_t... I>
 PyObject* invoke(PyObject* const* a, Py_ssize_t n, std::index_sequence<I...>) {
   const Entry& e = entries[WHICH];
-  if (e.at == nullptr) return PyErr_Format(PyExc_RuntimeError, "%s is not bound", e.name);
   if (n != (Py_ssize_t)sizeof...(A))
     return PyErr_Format(PyExc_TypeError, "%s takes %zd arguments, got %zd", e.name,
                         (Py_ssize_t)sizeof...(A), n);
+  if (e.at == nullptr) return PyErr_Format(PyExc_RuntimeError, "%s is not bound", e.name);
   const std::tuple<A...> args{(PyErr_Occurred() ? A() : taken<A>(a[I]))...};
   if (PyErr_Occurred()) return nullptr;
   int rc;

@@ -41,3 +41,12 @@ def test_sources_alone_build_and_load_in_one_process(sources):
               "print('from', m.__file__)\n", sources)
     assert out.returncode == 0, out.stdout + out.stderr
     assert f"from {sources}" in out.stdout
+
+
+def test_the_extension_counts_arguments_before_it_is_bound():
+    out = run("import combine_moe_dispatch_layout_amd as m\n"
+              "try:\n"
+              "    m._binding.moe_route(1, 2)\n"
+              "except TypeError as e:\n"
+              "    print('raised:', e)\n", ROOT)
+    assert "raised: moe_route takes 16 arguments" in out.stdout, out.stdout + out.stderr
