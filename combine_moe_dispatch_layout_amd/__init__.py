@@ -139,7 +139,9 @@ def __getattr__(name: str):
 
 
 def load_library() -> ctypes.CDLL:
-    """Load the HIP library; raises if it has not been built."""
+    """Load the HIP library; raises if it has not been built.  (The binding's
+    extension is asked for by the entry points that use it: moe_rms_norm,
+    moe_router_logits, moe_route and their gradients.)"""
     global _lib
     if _lib is not None:
         return _lib
@@ -209,8 +211,11 @@ def load_library() -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    binding = _extension()
-    for name in _FAST_CALLS:  # the same functions, called without ctypes
+    try:
+        binding = _extension()
+    except ImportError:  # the entry points that use it raise it; the others work
+        binding = None
+    for name in _FAST_CALLS if binding else ():  # the same functions, called without ctypes
         binding.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
         setattr(lib, name, getattr(binding, name))
     _lib = lib

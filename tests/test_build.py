@@ -4,6 +4,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 import pytest
 
@@ -50,3 +51,28 @@ def test_the_extension_counts_arguments_before_it_is_bound():
               "except TypeError as e:\n"
               "    print('raised:', e)\n", ROOT)
     assert "raised: moe_route takes 16 arguments" in out.stdout, out.stdout + out.stderr
+
+
+@pytest.mark.parametrize("left", ["none", "one that cannot be loaded"])
+def test_the_library_loads_without_the_extension(sources, left):
+    """What does not use the extension works without it; what does says what is
+    wrong with it."""
+    shutil.copy(os.path.join(ROOT, PACKAGE, "libmoe_dispatch.so"), sources / PACKAGE)
+    if left != "none":
+        name = "_binding" + sysconfig.get_config_var("EXT_SUFFIX")
+        (sources / PACKAGE / name).write_bytes(b"no shared object")
+    out = run("import torch, combine_moe_dispatch_layout_amd as m\n"
+              "assert m.load_library().moe_abi_version() > 0\n"
+              "assert m.moe_dispatch_capacity(4, 2, 8, 128) == 8 * 128\n"
+              "assert m.moe_router_logits_workspace_size(1, 64, 8) == 0\n"
+              "x = torch.zeros((3, 64), dtype=torch.bfloat16)\n"
+              "for call in (lambda: m.moe_rms_norm(x, x[0]), lambda: m.moe_route(x, 2),\n"
+              "             lambda: m.moe_router_logits(x, x)):\n"
+              "    try:\n"
+              "        call()\n"
+              "    except ImportError as e:\n"
+              "        print('raised:', e)\n", sources)
+    assert out.returncode == 0, out.stderr
+    said = "is missing: build it" if left == "none" else name
+    lines = out.stdout.splitlines()
+    assert len(lines) == 3 and all("raised:" in x and said in x for x in lines), out.stdout
