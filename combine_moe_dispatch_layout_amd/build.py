@@ -76,13 +76,7 @@ def _build_binding(verbose: bool) -> None:
     os.replace(tmp, BINDING)
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every source, link the shared library and the binding's
-    extension; returns the library's path."""
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
-        binding = pool.submit(_build_binding, verbose)
-        objs = list(pool.map(lambda s: _compile(s, verbose), SOURCES))
-        binding.result()
+def _link(objs: list, verbose: bool) -> None:
     tmp = LIB + f".tmp{os.getpid()}"
     exports = os.path.join(CSRC, "exports.map")  # only the moe_* C ABI is exported
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC",
@@ -91,6 +85,16 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source, link the shared library and the binding's
+    extension; returns the library's path."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        binding = pool.submit(_build_binding, verbose)
+        objs = list(pool.map(lambda s: _compile(s, verbose), SOURCES))
+        _link(objs, verbose)  # before the extension is asked for: the C ABI needs none
+        binding.result()
     return LIB
 
 

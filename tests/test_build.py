@@ -76,3 +76,19 @@ def test_the_library_loads_without_the_extension(sources, left):
     said = "is missing: build it" if left == "none" else name
     lines = out.stdout.splitlines()
     assert len(lines) == 3 and all("raised:" in x and said in x for x in lines), out.stdout
+
+
+def test_the_library_is_linked_whether_or_not_the_extension_compiles(sources):
+    """A user of the C ABI needs no C++ compiler that knows Python and torch;
+    that the extension was not made is an error all the same.  (A stand-in for
+    hipcc writes the file it is asked for.)"""
+    hipcc = sources / "hipcc"
+    hipcc.write_text("#!/bin/sh\n"
+                     "while [ \"$1\" != -o ]; do shift; done\n"
+                     "echo made > \"$2\"\n")
+    hipcc.chmod(0o755)
+    out = run("from combine_moe_dispatch_layout_amd import build\n"
+              "build.build()\n", sources,
+              {"HIPCC": str(hipcc), "CXX": str(sources / "no-such-compiler")})
+    assert out.returncode != 0 and "no-such-compiler" in out.stderr, out.stderr
+    assert (sources / PACKAGE / "libmoe_dispatch.so").read_text() == "made\n"
