@@ -49,6 +49,10 @@ constexpr float kFltMax = 3.40282347e38f;
 constexpr float kSigmoidError = 8e-7f;
 constexpr float kSoftmaxError = 2.8e-6f;
 constexpr float kSumError = 1.3e-7f;
+// A group's score of two keys is off by both's errors, and by roundings at the
+// size of the keys, not of their sum, which may cancel: 2^-24 of |one| + |two| for
+// the keys', the sum's, and that of taking this error off.
+constexpr float kGroupError = 2e-7f;
 // A sum of such exponentials: their 2.4e-7, and the rounding of each argument, whose
 // size is at most log E = 6.3 where averaged by the terms' shares.
 constexpr double kShareError = 7e-7;
@@ -271,6 +275,24 @@ __device__ __forceinline__ void join_two(float& one, float& two) {
   one = fmaxf(one, o);
 }
 
+// A group's score, and by how much it may be off.
+struct GroupScore {
+  float of, error;
+  __device__ __forceinline__ GroupScore(const float2& two, bool by_two, float score_error) {
+    const bool both = by_two && two.y > -__builtin_inff();
+    of = both ? two.x + two.y : two.x;
+    error = score_error + kGroupError * (fabsf(two.x) + (both ? fabsf(two.y) : 0.0f));
+  }
+  // What it is at least and at most (anything, where the sizes leave fp32).
+  __device__ __forceinline__ float low() const {
+    return error < __builtin_inff() ? of - error : -__builtin_inff();
+  }
+  __device__ __forceinline__ float high() const {
+    if (of == -__builtin_inff()) return of;  // no expert is left
+    return error < __builtin_inff() ? of + error : __builtin_inff();
+  }
+};
+
 // The groups that stay, of a row whose keys lie in `keys`: bit g << shift for
 // group g.  `near`: a group that stays and one that does not are too near to
 // tell.
@@ -292,9 +314,6 @@ __device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const float*
     }
     return float2{one, two};
   };
-  const auto score_of = [&](float one, float two) {
-    return a.by_two && two > -inf ? one + two : one;
-  };
   uint64_t kept = 0;
   float least = inf, most = -inf;
   shift = 0;
@@ -308,7 +327,8 @@ __device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const float*
     if (shift > 1) join_two<0x4E>(x, y);   // quad_perm 2 3 0 1
     if (shift > 2) join_two<0x141>(x, y);  // row_half_mirror
     if (shift > 3) join_two<0x140>(x, y);  // row_mirror
-    const float of = score_of(x, y);
+    const GroupScore mine(float2{x, y}, a.by_two, score_error);
+    const float of = mine.of;
     int rank = 0;
     for (int j = 0; j < a.groups; ++j) {
       const float o = LANES == kWave ? of_lane(of, j << shift) : __shfl(of, j << shift, LANES);
@@ -316,16 +336,18 @@ __device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const float*
     }
     const bool stays = g < a.groups && rank < a.top_groups && of > -inf;
     kept = __ballot(stays) >> first;
-    if (stays) least = of;
-    if (g < a.groups && !stays) most = of;
+    if (stays) least = mine.low();
+    if (g < a.groups && !stays) most = mine.high();
   } else {  // more groups than lanes: several a lane
     constexpr int kRounds = kMaxGroups / LANES;
-    float of[kRounds];
+    float of[kRounds], low[kRounds], high[kRounds];
     int rank[kRounds] = {};
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
-      const float2 two = best_two(lane + r * LANES, 0, 1);
-      of[r] = score_of(two.x, two.y);
+      const GroupScore mine(best_two(lane + r * LANES, 0, 1), a.by_two, score_error);
+      of[r] = mine.of;
+      low[r] = mine.low();
+      high[r] = mine.high();
     }
 #pragma unroll
     for (int q = 0; q < kRounds; ++q)
@@ -343,16 +365,14 @@ __device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const float*
       if (LANES < kWave) bits &= (uint64_t(1) << (LANES % kWave)) - 1;
       kept |= bits << (r * LANES % 64);
       if (stays)
-        least = fminf(least, of[r]);
+        least = fminf(least, low[r]);
       else
-        most = fmaxf(most, of[r]);
+        most = fmaxf(most, high[r]);
     }
   }
   least = over_row<LANES, Min>(least);
   most = over_row<LANES, Max>(most);
-  // (A sum of two keys is off by both's errors and a rounding.)
-  const float error = 2.0f * (score_error + kSumError * fabsf(least));
-  near = score_error > 0.0f && most > -inf && !(least - most > error);
+  near = score_error > 0.0f && most > -inf && !(least > most);
   return kept;
 }
 
