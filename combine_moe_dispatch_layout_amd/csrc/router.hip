@@ -493,9 +493,10 @@ __global__ __launch_bounds__(WAVES* kWave) void shared_k_kernel(const SharedK p)
 // ---- the parts of dl -----------------------------------------------------------------
 // Two values' three bf16 parts, that of the second in the upper half.  The first
 // is the value cut to 8 bits (so that none rounds up to infinity), the second
-// what is left rounded to 8, the third the rest, which has no more than 8.  An
-// infinity is all in the first; a NaN, whose mark the cut may lose, is in the
-// others too.
+// what is left rounded to 8, the third the rest, which has no more than 8.  (Of
+// values below 2^-110 that rest ends below 2^-133, bf16's smallest step, and is
+// rounded to it.)  An infinity is all in the first; a NaN, whose mark the cut may
+// lose, is in the others too.
 __device__ __forceinline__ void pair_parts(float a, float b, uint32_t& hi, uint32_t& mid,
                                            uint32_t& lo) {
   const uint32_t up = __float_as_uint(a), vp = __float_as_uint(b);
