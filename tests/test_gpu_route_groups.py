@@ -80,3 +80,40 @@ def test_group_scores_that_leave_fp32(moe, score, bs):
     check(moe, l, bias, 4, score=score, groups=8, top_groups=2)
     bias[40] = float("inf")
     check(moe, l, bias, 4, score=score, groups=8, top_groups=3)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bs,e,k,groups,top", [(128, 256, 8, 8, 4), (4100, 512, 16, 16, 3),
+                                               (4099, 128, 5, 64, 9), (300, 60, 6, 6, 3)])
+def test_bf16_logits(moe, bs, e, k, groups, top, score):
+    """Logits of 8 bits: many keys and groups are equal, and go to the lowest."""
+    gen = torch.Generator().manual_seed(bs + e)
+    l = torch.randn((bs, e), generator=gen).bfloat16()
+    l[1::3] = (2 * l[1::3]).round() / 2
+    l[2::5] = l[2::5].masked_fill(torch.rand((len(l[2::5]), e), generator=gen) < 0.6,
+                                  float("-inf"))
+    few = 0.25 * torch.randint(-2, 3, (e,), generator=gen).float()
+    for group_score in ("top2", "max"):
+        for bias in (torch.zeros(e), few, 0.1 * torch.randn(e, generator=gen)):
+            check(moe, l, bias, k, score=score, groups=groups, top_groups=top,
+                  group_score=group_score)
+        ids, _ = moe.moe_route(l.to(DEV), k, score=score, groups=groups, top_groups=top,
+                               group_score=group_score)
+        want, _ = ref.route(l.float().numpy(), k, score=score, groups=groups, top_groups=top,
+                            group_score=group_score)
+        assert np.array_equal(ids.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [3.3, 30.0, 1000.0, 1e5])
+@pytest.mark.parametrize("bs,e,k", [(300, 24, 16), (4200, 64, 12), (500, 256, 16),
+                                    (4200, 512, 16)])
+def test_experts_far_below_the_best(moe, bs, e, k, size, score):
+    """Keys of another size than the largest one's, nearer to each other than
+    their own roundings."""
+    gen = torch.Generator().manual_seed(bs + e)
+    l = torch.randn((bs, e), generator=gen)
+    for most, rest in ((0.0, -size), (size, 0.0), (size, -size)):
+        bias = rest + 1e-7 * size * torch.randn(e, generator=gen)
+        bias[::7] = most + 0.1 * torch.randn(len(bias[::7]), generator=gen)
+        check(moe, l, bias, k, score=score)
