@@ -66,6 +66,37 @@ __device__ __forceinline__ float exp_f32(float x) {
   return __builtin_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
 }
 
+// The k chosen experts' scores are made in 64 bits, and weights and gradients
+// rounded once: one value a lane, little beside the choice (us, in 32 bits and so:
+// 16384 x 512 softmax 9.1, 9.1, its gradient with sigmoid 13.4, 13.6; 777 x 60's
+// gradient 3.2, 3.3; weights' error 5.5e-8, 2.5e-8).  A sum over all experts is one
+// of fp32 exponentials: the gradient through it takes 18.4 for 16384 x 512 as it is.
+//
+// e^x to 2^-32 of itself: x = n log 2 + r, and r's Taylor series to its 8th power
+// (|r| <= 0.347, so what is left out is below 0.347^9 / 9! = 2e-10).
+__device__ __forceinline__ double exp_f64(double x) {
+  x = fmin(fmax(x, -700.0), 700.0);  // past what an fp32 result can tell
+  const double n = __builtin_rint(x * 1.4426950408889634074);
+  const double r = __builtin_fma(n, -0.69314718055994530942, x);
+  double e = 1.0 / 40320;
+  e = __builtin_fma(e, r, 1.0 / 5040);
+  e = __builtin_fma(e, r, 1.0 / 720);
+  e = __builtin_fma(e, r, 1.0 / 120);
+  e = __builtin_fma(e, r, 1.0 / 24);
+  e = __builtin_fma(e, r, 1.0 / 6);
+  e = __builtin_fma(e, r, 0.5);
+  e = __builtin_fma(e, r, 1.0);
+  e = __builtin_fma(e, r, 1.0);
+  return __builtin_ldexp(e, (int)n);
+}
+
+// 1 / x, x a normal number: the reciprocal instruction's (off by 2^-24 of itself,
+// measured), whose error a step of Newton's squares.
+__device__ __forceinline__ double inverse(double x) {
+  const double y = __builtin_amdgcn_rcp(x);
+  return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+}
+
 // A logit as it counts: a NaN or -inf masks the expert, +inf is the largest
 // finite value.
 __device__ __forceinline__ float counted(float l) {
@@ -115,40 +146,50 @@ __device__ __forceinline__ void read_bias(const RouteArgs& a, int lane, float (&
   }
 }
 
+// A row's sum: few additions in turn round in 32 bits (kSoftmaxError), and
+// independently in each of four parts of a lane; the parts are added in 64.
+template <int LANES, int PER>
+__device__ __forceinline__ double row_sum(const float (&v)[PER]) {
+  float four[4] = {};
+#pragma unroll
+  for (int i = 0; i < PER; ++i) four[i % 4] += v[i];
+  return over_row<LANES, Sum>(((double)four[0] + four[1]) + ((double)four[2] + four[3]));
+}
+
 __device__ __forceinline__ bool masked(float l) { return l == -__builtin_inff(); }
 
 // The chosen experts' weights (before the scaling): lane j of the row holds the
-// logit of the j-th.  Softmax without renormalisation needs the row's largest
-// logit and the sum of its exponentials.
-template <int LANES>
-__device__ __forceinline__ float weight_of(const RouteArgs& a, float l, bool real, float top,
-                                           float sum) {
+// logit of the j-th (k <= 16: in the row's first 16 lanes).  Softmax without
+// renormalisation needs the row's largest logit and the sum of its exponentials.
+__device__ __forceinline__ double weight_of(const RouteArgs& a, float l, bool real, float top,
+                                            double sum) {
   if (!a.renormalize) {
-    if (!real) return 0.0f;
-    return a.sigmoid ? 1.0f / (1.0f + exp_f32(-l)) : exp_f32(l - top) / sum;
+    if (!real) return 0.0;
+    return a.sigmoid ? inverse(1.0 + exp_f64(-(double)l))
+                     : exp_f64((double)l - top) * inverse(sum);
   }
-  const float most = over_row<LANES, Max>(real ? l : -__builtin_inff());
-  float t = 0.0f;
+  const float most = over_row<16, Max>(real ? l : -__builtin_inff());
+  double t = 0.0;
   if (real) {
     if (a.sigmoid) {
       // Scores times e^-c, so that the largest is at least 1/2.
-      const float c = fminf(most, 0.0f);
-      t = 1.0f / (exp_f32(c) + exp_f32(c - l));
+      const double c = fminf(most, 0.0f);
+      t = inverse(exp_f64(c) + exp_f64(c - l));
     } else {
-      t = exp_f32(l - most);
+      t = exp_f64((double)l - most);
     }
   }
-  const float total = over_row<LANES, Sum>(t);
-  return real ? t / total : 0.0f;
+  const double total = over_row<16, Sum>(t);
+  return real ? t * inverse(total) : 0.0;
 }
 
 template <int LANES>
 __device__ __forceinline__ void write_choice(const RouteArgs& a, int64_t row, int lane, int id,
-                                             float l, float top, float sum) {
-  const float w = a.scale * weight_of<LANES>(a, l, id >= 0, top, sum);
+                                             float l, float top, double sum) {
+  const double w = a.scale * weight_of(a, l, id >= 0, top, sum);
   if (lane < a.k) {
     a.ids[row * a.k + lane] = id;
-    a.scales[row * a.k + lane] = w;
+    a.scales[row * a.k + lane] = (float)w;
   }
 }
 
@@ -257,11 +298,12 @@ __device__ __forceinline__ void route_exactly(const RouteArgs& a, int64_t row, d
       chosen = of;
     }
   }
-  float sum = 0.0f;
+  double sum = 1.0;
   if (!a.sigmoid && !a.renormalize) {
+    float of[kWavePer];
 #pragma unroll
-    for (int i = 0; i < kWavePer; ++i) sum += exp_f32(l[i] - (masked(top) ? 0.0f : top));
-    sum = over_row<kWave, Sum>(sum);
+    for (int i = 0; i < kWavePer; ++i) of[i] = exp_f32(l[i] - (masked(top) ? 0.0f : top));
+    sum = row_sum<kWave>(of);
   }
   write_choice<kWave>(a, row, lane, id, chosen, top, sum);
 }
@@ -404,12 +446,12 @@ __global__ __launch_bounds__(kThreads, 4) void route_kernel(const RouteArgs a) {
   for (int i = 0; i < PER; ++i) top = fmaxf(top, key[i]);
   float most = top;  // of the lane
   top = over_row<LANES, Max>(top);
-  float sum = 1.0f;
+  double sum = 1.0;
   if (sums) {
-    float four[4] = {};  // few additions in turn: kSoftmaxError
+    float of[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) four[i % 4] += exp_f32(key[i] - (masked(top) ? 0.0f : top));
-    sum = over_row<LANES, Sum>((four[0] + four[1]) + (four[2] + four[3]));
+    for (int i = 0; i < PER; ++i) of[i] = exp_f32(key[i] - (masked(top) ? 0.0f : top));
+    sum = row_sum<LANES>(of);
   }
   bool near = false;
   float score_error = 0.0f;
@@ -418,7 +460,7 @@ __global__ __launch_bounds__(kThreads, 4) void route_kernel(const RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) l[i] = key[i];
     if (by_score) {
-      const float by = 1.0f / sum;
+      const float by = 1.0f / (float)sum;
       score_error = a.sigmoid ? kSigmoidError : kSoftmaxError * by;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
@@ -635,29 +677,30 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteArgs a) {
       if (masked(of)) id = -1;
     }
   }
-  float p[PER], top = -__builtin_inff(), sum = 1.0f;
+  float p[PER], top = -__builtin_inff();
+  double sum = 1.0;
   if (all) {
     read_row<LANES, PER, BF16>(a, row, lane, p);
 #pragma unroll
     for (int i = 0; i < PER; ++i) top = fmaxf(top, p[i]);
     top = over_row<LANES, Max>(top);
-    sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      p[i] = masked(p[i]) ? 0.0f : exp_f32(p[i] - top);
-      sum += p[i];
-    }
-    sum = over_row<LANES, Sum>(sum);
+    for (int i = 0; i < PER; ++i) p[i] = masked(p[i]) ? 0.0f : exp_f32(p[i] - top);
+    sum = row_sum<LANES>(p);
   }
   const bool real = id >= 0;
-  const float q = weight_of<LANES>(a, of, real, top, sum);
-  const float dot = over_row<LANES, Sum>(real ? g * q : 0.0f);
+  const double q = weight_of(a, of, real, top, sum);
+  const double dot = over_row<16, Sum>(real ? g * q : 0.0);
   float d = 0.0f;
   if (real) {
-    d = a.renormalize ? q * (g - dot) : q * g;
-    if (a.sigmoid) d /= 1.0f + exp_f32(of);
+    double v = a.renormalize ? q * (g - dot) : q * g;
+    if (a.sigmoid) v *= inverse(1.0 + exp_f64(of));
+    d = (float)(a.scale * v);
   }
-  const float by = sum > 0.0f ? dot / sum : 0.0f;  // nothing left: no gradient
+  // Of every expert's score; nothing left: no gradient.  (Lane 0's: other lanes
+  // past the first 16 have no chosen expert's.)
+  const float by =
+      sum > 0.0 ? __shfl((float)(a.scale * dot * inverse(sum)), 0, LANES) : 0.0f;
   float v[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) v[i] = all ? -p[i] * by : 0.0f;
@@ -674,9 +717,9 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteArgs a) {
     if (e >= a.num_experts) continue;
     const int64_t to = row * a.grad_logits_stride + e;
     if (BF16)
-      static_cast<uint16_t*>(a.grad_logits)[to] = (uint16_t)f32_to_bf16_rne(a.scale * v[i]);
+      static_cast<uint16_t*>(a.grad_logits)[to] = (uint16_t)f32_to_bf16_rne(v[i]);
     else
-      static_cast<float*>(a.grad_logits)[to] = a.scale * v[i];
+      static_cast<float*>(a.grad_logits)[to] = v[i];
   }
 }
 

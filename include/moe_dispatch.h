@@ -730,7 +730,9 @@ int moe_router_logits_backward(const float* grad_logits, int64_t grad_logits_str
  * rounding of fp32 scores.  An expert whose logit is -inf or NaN, or whose
  * bias is -inf or NaN, is never chosen (without renormalize, a softmax's sum
  * still counts an expert that only its bias excludes); +inf counts as the
- * largest finite value.  Where fewer than k experts are left, the remaining
+ * largest finite value.  expert_scales are made in 64 bits and rounded once;
+ * without renormalize a softmax divides by a sum of fp32 exponentials, off by
+ * less than 2^-19 of itself.  Where fewer than k experts are left, the remaining
  * expert_ids are -1 and their expert_scales 0: pairs that every call drops.
  *
  *  logits         in  [bs, num_experts], fp32 or bf16 (logits_dtype MOE_FP32
@@ -759,7 +761,10 @@ int moe_route(const void* logits, int32_t logits_dtype, int64_t logits_stride,
  *   sigmoid                   scale * s_j * (1 - s_j) * g_j        at e = id_j
  *   sigmoid, renormalize      scale * q_j * (1 - s_j) * (g_j - G)  at e = id_j
  *
- * and 0 elsewhere, in fp32, rounded once if the logits are bf16.  Ids outside
+ * and 0 elsewhere.  What is there at e = id_j is made in 64 bits and rounded
+ * once to fp32; the first line's other terms are products of fp32 exponentials
+ * (a few 2^-24 of a term beside the rounding of l[e] - max l).  Rounded to bf16
+ * if the logits are.  Ids outside
  * [0, num_experts), or of an expert whose logit is -inf or NaN, count as
  * none; an id that occurs twice counts twice.
  *
