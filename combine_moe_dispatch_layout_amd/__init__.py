@@ -1285,8 +1285,9 @@ def moe_router_logits_backward(grad_logits: torch.Tensor, x: Optional[torch.Tens
     """Gradient of moe_router_logits: ``(grad_x, grad_weight)`` from grad_logits
     [BS, E] fp32.  grad_x bf16 [BS, H] includes grad_x_add (what reaches the
     token on other paths, moe_dispatch_backward's result; grad_x may be given
-    as grad_x_add itself), grad_weight is fp32 [E, H].  An output not needed is
-    None; without need_weight x may be None."""
+    as grad_x_add itself), grad_weight is fp32 [E, H].  grad_x takes the upper 16
+    of grad_logits' 24 bits, grad_weight all.  An output not needed is None;
+    without need_weight x may be None."""
     dev, bs, experts, gs, g_at = _matrix(grad_logits, _F32, "grad_logits")
     rows, hidden, w_at = _router_weight(weight, None, dev)
     if rows != experts:

@@ -7,7 +7,12 @@
 // w are bf16, so the forward's products are exact.  dl is fp32: it is split
 // once into three bf16 parts that add up to it exactly (8 + 8 + 8 bits), and
 // the gradients add the parts' products: two for dx, which is rounded to 8 bits
-// itself (what is left out is below 2^-15 of a term), all three for dw.
+// itself, all three for dw.  What dx leaves out is at most 2^-16 of a term (the
+// first part leaves less than 2^-7 of it, of which the second's rounding leaves
+// 2^-9).  With the third 4 in 10000 of its values come out a step of bf16 apart, the
+// error against 64 bits stays the same to four digits, and dx of 4096 tokens of 7168
+// channels takes on 64, 128, 256 and 512 experts 28, 34, 89 and 99 us in place of 27,
+// 31, 42 and 75.
 //
 // router_kernel is a product of tiles, D[j, i] = sum_p sum_k J_p[j, k] * I[i, k].  An
 // operand lies in memory either by rows (k neighbouring) or by columns (i or j

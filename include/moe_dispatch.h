@@ -685,7 +685,11 @@ int moe_router_logits(const void* x, int64_t x_stride, const void* weight, int32
  *   grad_weight[e, h] = sum_t grad_logits[t, e] * x[t, h]       (fp32)
  *
  * grad_x_add is what reaches the token on other paths (moe_dispatch_backward's
- * grad_x).
+ * grad_x).  Sums are fp32.  grad_logits enter grad_weight with all of their 24
+ * bits (down to 2^-133) and grad_x, which is rounded to 8 itself, with 16: a
+ * term of grad_x is off by at most 2^-16 of its magnitude, also where the terms
+ * cancel.  They enter in parts, so where the formula makes an infinity of one
+ * in weight or x and a finite grad_logits, the result may be a NaN.
  *
  *  grad_logits    in  fp32 [bs, num_experts], row stride grad_logits_stride.
  *  x              in  as for moe_router_logits (read for grad_weight only).

@@ -114,3 +114,34 @@ def test_both_sides_of_each_change(moe, bs, h, e):
     odd.copy_(g)
     assert torch.equal(moe.moe_router_logits_backward(odd, x, w, need_x=False)[1], dw)
     assert torch.equal(moe.moe_router_logits_backward(odd, x, w, need_weight=False)[0], dx)
+
+
+@pytest.mark.parametrize("bs,h,e", [(20, 96, 24), (300, 96, 24), *SIZES[2:3]])
+def test_infinite_rows_and_weights_spoil_what_they_enter_alone(moe, bs, h, e):
+    """An infinity in x or weight gives an infinity or a NaN, and nothing else."""
+    x, g = torch.ones((bs, h)), torch.ones((bs, e))
+    w = torch.ones((e, h))
+    x[3, 5], w[2, 7] = float("inf"), float("-inf")
+    g[3, 0] = 1.7e-3     # three parts
+    dx, dw = moe.moe_router_logits_backward(g.to(DEV), x.bfloat16().to(DEV), w.bfloat16().to(DEV))
+    dx, dw = dx.cpu().float(), dw.cpu()
+    assert not dw[:, 5].isfinite().any() and not dx[:, 7].isfinite().any()
+    dw[:, 5], dx[:, 7] = bs, e
+    assert (dw[1:] == bs).all() and (dx[[0, 1, 2, 4]] == e).all()
+
+
+@pytest.mark.parametrize("bs,h,e", [(1, 64, 8), (40, 256, 60), (5000, 256, 60), (4200, 512, 256),
+                                    (2000, 512, 512)])
+def test_terms_of_the_rows_gradient_that_cancel(moe, bs, h, e):
+    """Pairs of experts with one weight and all but opposite gradients: what is
+    lost is held to 2^-16 of the terms' magnitudes and the fp32 sums' rounding."""
+    gen = torch.Generator().manual_seed(bs + e)
+    w = torch.randn((e // 2, h), generator=gen).bfloat16().repeat_interleave(2, 0)
+    g = torch.randn((bs, e // 2), generator=gen).repeat_interleave(2, 1)
+    g[:, 1::2] *= -(1 - 2.0 ** -18)
+    x = torch.zeros((bs, h), dtype=torch.bfloat16, device=DEV)
+    dx, _ = moe.moe_router_logits_backward(g.to(DEV), x, w.to(DEV), need_weight=False)
+    want = g.double() @ w.double()
+    mag = g.double().abs() @ w.double().abs()
+    bound = 2.0 ** -8 * want.abs() + 1.01 * (2.0 ** -16 + (2 * e + 64) * 2.0 ** -23) * mag
+    assert ((dx.cpu().double() - want).abs() <= bound).all()
