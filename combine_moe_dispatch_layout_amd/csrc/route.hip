@@ -20,9 +20,11 @@
 // expert, the lowest index among equals.  Each lane sorts its 4 best, and k
 // rounds take the minimum over the lanes' first ones.
 //
-// Measured: 16384 rows of 512 logits, softmax, best 8, 10.5 us (33 MB, 3.3 TB/s: a row's
-// instructions bound it); 128 rows of 256 with a bias and 8 groups 5.7; the gradient of
-// 16384 rows of 512 12.8 (5.3 TB/s), of 777 of 60 3.8.  An empty launch is 2.2.
+// Measured: 16384 rows of 512 logits, softmax, best 8, 9.1 us in a graph (33 MB, 3.6
+// TB/s).  Instructions bound it: a wave's four rows take 829 vector ones, which of 4
+// waves a SIMD at 4 cycles each are 5.5 us, beside a launch's 2.2 and the loads that
+// come first.  128 rows of 256 with a bias and 8 groups 5.1; the gradient of 16384 rows
+// of 512 13.6 (5.0 TB/s), of 777 of 60 3.3.
 //
 // Where neighbours in that order are nearer to each other than the numbers can
 // tell (23 bits, and the rounding of fp32 scores), the candidates are compared

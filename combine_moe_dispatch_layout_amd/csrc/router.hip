@@ -27,8 +27,8 @@
 // The other kernels are for what that one does badly: one_token_kernel and
 // shared_k_kernel for few tokens or experts, few_grad_w for their dw,
 // small_grad_x_kernel for their dx (128 of 7168 on 256 7 us) and grad_x_kernel for
-// dx of many, whose k is short (4096 of 7168 on 256 43 us: the start with
-// dl 9, products 28, the memory of add and dx the rest).
+// dx of many, whose k is short (4096 of 7168 on 256 42 us, 45 to 49 beside the
+// parts of dl: the start with dl 9, products 28, the memory of add and dx the rest).
 #include "lds_loads.h"
 #include "moe_internal.h"
 
